@@ -1,0 +1,820 @@
+// attn_cache.cu - attention of new query rows over a key/value cache held in
+// 8 bits: blocks of bt tokens, e4m3 numbers times one scale per block, head
+// and side (keys, values), found through a block table.
+//
+// For head j of batch item b, key row k8 and value row v8 of position p in a
+// block with scales ks, vs:
+//   s = c ks (q . k8),   z = sum_p softmax_p(s) vs v8.
+// The keys are folded 16 at a time (a block holds a whole number of such
+// groups, so ks and vs are uniform in one) into the summary (m, l, z) of
+// "Stable summary of an attention key block" (alphabetamath.cc, Definition):
+// the group is summarised on its own, (m_g, l_g, a_g = sum 2^{s - m_g} v8), and
+// merged, z' = 2^{m - m'} z + 2^{m_g - m'} vs a_g. Scores are in base 2.
+//
+// Bound. 2 (d_h + d_vh) flop per query row and byte of the cache: with up to
+// 16 rows per key/value head (new rows times the query heads that share it)
+// the cache is streamed once and memory is the bound.
+//
+// Work split. The 8-bit rows of every (batch item, key/value head, tile of 16
+// rows) form one list of groups of SK keys; warp w of all W warps takes the
+// equal contiguous range [w G / W, (w + 1) G / W) whatever the lengths, which
+// the kernel reads on the device. A range that covers a tile's keys whole
+// writes z / l; otherwise each piece's summary goes to the workspace and
+// cache_merge_kernel merges a tile's pieces in order. No warp waits for
+// another one.
+//
+// Products. mma.sync m16n8k16 in fp16 with fp32 sums, straight from the bytes:
+// e4m3 is a subset of fp16 (cvt.rn.f16x2.e4m3x2 is exact), a query row is
+// scaled by a power of two that brings its largest element to [2^14, 2^15),
+// so bf16 queries are exact down to 2^-28 of the row's largest, and the
+// weights 2^{s - m_g} <= 1 by 2^14. fp32 queries and weights are taken as the
+// sum of two fp16 numbers (22 bits). At 16 rows the tensor pipe is far from
+// being the bound, so the small mma.sync tile, whose operands come from
+// registers, fits better than tcgen05's 128 rows.
+//
+// Order of the columns. In q . k8 the index over d may be permuted, so lane
+// (g, t) reads its share of key row g as 16 consecutive bytes; in sum p v8 the
+// index over d of the output tiles may be, so it reads 16 consecutive bytes
+// of each of its four value rows and turns 4 x 4 bytes by byte permutes. The
+// 16-byte pieces of a row are stored XOR-swizzled so that these reads meet no
+// bank twice.
+//
+// Copies. Each warp keeps a ring of stages of its own (cp.async, 16 bytes per
+// lane), filled ahead of the arithmetic across tile and sequence borders.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "device_common.cuh"
+#include "internal.h"
+
+namespace mha {
+namespace {
+
+constexpr int CA_WARPS = 8;
+constexpr int CA_THREADS = 32 * CA_WARPS;
+constexpr int CA_MAX_CTAS = 192;   // of the main kernel: bounds the workspace
+constexpr int CA_HEADER = 8192;    // workspace: first group of every batch item
+constexpr int CM_THREADS = 128;    // merge kernel
+
+struct CacheAttnParams {
+  const void* Q;        // (B, h, n_q, d_h)
+  const uint8_t* K;     // (n_blocks, h_kv, bt, d_h)
+  const uint8_t* V;     // (n_blocks, h_kv, bt, d_vh)
+  const float* Ks;      // (n_blocks, h_kv)
+  const float* Vs;
+  const int32_t* table; // (B, max_blocks)
+  const int32_t* total; // (B)
+  const int32_t* fresh; // (B) or null: new rows, n_q
+  void* Z;              // (B, n_q, h d_vh)
+  int32_t* first;       // workspace: (B + 1) groups before item b, per tile of rows
+  float* part;          // workspace: summaries, [2 W][slot_rows][2 + d_vh]
+  int32_t* err;
+  int B, n_q, h, h_kv, share, d_h, d_vh, n_blocks, bt, max_blocks;
+  int tiles;            // tiles of 16 rows per key/value head
+  int slot_rows;        // rows of a summary slot: min(16, n_q share)
+  int causal_tail;
+  int warps;            // W
+  float cl2;            // c log2(e)
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(full ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Two e4m3 numbers (the low or high half of w) as two fp16 numbers, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two floats as fp16 (hi), and what that rounding left out as fp16 (lo).
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t rest_half(float a, float b, uint32_t hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_half(a - f.x, b - f.y);
+}
+
+// The rows of a batch item: keys in the cache and new query rows, each held
+// inside its bounds.
+struct Item {
+  int total, fresh;
+};
+__device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& bad) {
+  const int t = __ldg(P.total + b), f = P.fresh ? __ldg(P.fresh + b) : P.n_q;
+  const int most = P.max_blocks * P.bt;
+  bad = t < 0 || t > most || f < 0 || f > P.n_q;
+  return Item{min(max(t, 0), most), min(max(f, 0), P.n_q)};
+}
+
+// Stage layout for rows of D bytes: SK key rows, SK value rows, then per
+// 16-key group {ks, vs, valid, 0}.
+template <int D>
+struct Stage {
+  static constexpr int SK = D == 256 ? 16 : 32;  // keys
+  static constexpr int SUBS = SK / 16;
+  static constexpr int ROWS = SK * D;            // bytes of one side
+  static constexpr int BYTES = 2 * ROWS + 16 * SUBS;
+  static constexpr int N = D == 64 ? 6 : 3;      // stages per warp
+  static constexpr int SMEM = CA_WARPS * N * BYTES + (MHA_MAX_PADDED_BATCH + 8) * 4;
+};
+
+// Byte offset of 16-byte piece c of row k, swizzled: the reads of eight lanes
+// at a time (key rows 2p, 2p + 1 and four neighbouring pieces; or value rows
+// 0, 2, 4, 6 or 1, 3, 5, 7 and two neighbouring pieces) touch each bank once.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int k, int c) {
+  if constexpr (D == 64) {
+    const int line = k >> 1;
+    return (uint32_t)(line * 128 + (((((k & 1) << 2) | c) ^ ((line & 3) << 1)) << 4));
+  } else {
+    const int f = (k & 2) | (((k ^ (k >> 2)) & 1) << 2);
+    return (uint32_t)(k * D + ((c & 8) << 4) + (((c & 7) ^ f) << 4));
+  }
+}
+
+// Where a warp is in the list of groups.
+struct Cursor {
+  int b, pr, gi, ng;  // batch item, tile of rows in it, group in that, groups per tile
+};
+
+template <int D, int RH, bool F32>
+__global__ void __launch_bounds__(CA_THREADS, 1)
+    cache_attention_kernel(const __grid_constant__ CacheAttnParams P) {
+  using S = Stage<D>;
+  constexpr int NT = D / 8;   // output tiles of 8 columns
+  constexpr int KC = D / 64;  // 16-byte pieces of a key row per lane
+  extern __shared__ __align__(128) unsigned char smem[];
+  int* first = reinterpret_cast<int*>(smem + CA_WARPS * S::N * S::BYTES);  // (B + 1)
+  __shared__ int warp_sums[CA_WARPS];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane >> 2, t = lane & 3;
+
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+
+  // groups per tile of every batch item, and their sums
+  {
+    constexpr int PER = MHA_MAX_PADDED_BATCH / CA_THREADS;
+    int n[PER], sum = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int b = threadIdx.x * PER + k;
+      n[k] = 0;
+      if (b < P.B) {
+        bool bad;
+        const Item it = item_of(P, b, bad);
+        if (bad && blockIdx.x == 0 && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+        if (it.fresh > 0) n[k] = (it.total + S::SK - 1) / S::SK;
+      }
+      sum += n[k];
+    }
+    int v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int before = v - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int b = threadIdx.x * PER + k;
+      if (b <= P.B) {
+        first[b] = before;
+        if (blockIdx.x == 0) P.first[b] = before;
+      }
+      before += n[k];
+    }
+    if (threadIdx.x == CA_THREADS - 1 && P.B == MHA_MAX_PADDED_BATCH) {
+      first[P.B] = before;
+      if (blockIdx.x == 0) P.first[P.B] = before;
+    }
+    __syncthreads();
+  }
+  const int unit = P.h_kv * P.tiles;
+  const long long G = (long long)first[P.B] * unit;
+  const int w = blockIdx.x * CA_WARPS + warp;
+  long long g0 = w * G / P.warps;
+  const long long g1 = (w + 1) * G / P.warps;
+  if (g0 >= g1) return;
+
+  Cursor cc;  // what is computed
+  {
+    int lo = 0, hi = P.B - 1;  // the last item that starts at or before g0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((long long)first[mid] * unit <= g0) lo = mid; else hi = mid - 1;
+    }
+    cc.b = lo;
+    cc.ng = first[lo + 1] - first[lo];
+    const long long in = g0 - (long long)first[lo] * unit;
+    cc.pr = (int)(in / cc.ng);
+    cc.gi = (int)(in - (long long)cc.pr * cc.ng);
+  }
+  Cursor lc = cc;  // what is loaded
+  long long left = g1 - g0, load_left = left;
+  auto advance = [&](Cursor& c) {
+    if (++c.gi < c.ng) return;
+    c.gi = 0;
+    if (++c.pr < unit) return;
+    c.pr = 0;
+    do {
+      ++c.b;
+    } while (c.b < P.B && first[c.b + 1] == first[c.b]);
+    c.ng = c.b < P.B ? first[c.b + 1] - first[c.b] : 1;
+  };
+
+  const uint32_t ring = smem_u32(smem) + warp * S::N * S::BYTES;
+  // table entries [win, win + 32) of item win_b, one per lane
+  int win = 0, win_b = -1, win_id = 0, load_total = 0;
+  auto issue = [&](int stage) {
+    const uint32_t dst = ring + stage * S::BYTES;
+    const int k0 = lc.gi * S::SK, kv = lc.pr / P.tiles;
+    const int j0 = k0 / P.bt, j1 = (k0 + S::SK - 1) / P.bt;
+    if (lc.b != win_b || j0 < win || j1 >= win + 32) {
+      if (lc.b != win_b) {
+        bool bad;
+        load_total = item_of(P, lc.b, bad).total;
+      }
+      win_b = lc.b;
+      win = j0;
+      const int j = win + lane;
+      win_id = j < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + j) : -1;
+    }
+#pragma unroll
+    for (int sub = 0; sub < S::SUBS; ++sub) {
+      const int k = k0 + 16 * sub, j = k / P.bt;
+      int id = __shfl_sync(0xffffffffu, win_id, j - win);
+      const bool used = k < load_total;
+      const bool ok = used && id >= 0 && id < P.n_blocks;
+      if (used && !ok && P.err && lane == 0) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+      if (!ok) id = 0;
+      const long long blk = (long long)id * P.h_kv + kv;
+      const int row = k - j * P.bt;
+      const uint8_t* ks = P.K + (blk * P.bt + row) * P.d_h;
+      const uint8_t* vs = P.V + (blk * P.bt + row) * P.d_vh;
+      constexpr int C = D / 16;        // pieces per row
+      constexpr int RPI = 32 / C;      // rows per instruction
+      const int c = lane % C, r0 = lane / C;
+      const int rows = ok ? min(16, load_total - k) : 0;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = r0 + i * RPI;
+        const bool in = r < rows;
+        const bool kin = in && c * 16 < P.d_h, vin = in && c * 16 < P.d_vh;
+        const uint32_t at = piece_at<D>(16 * sub + r, c);
+        cp_async16(dst + at, kin ? ks + (long long)r * P.d_h + c * 16 : P.K, kin);
+        cp_async16(dst + S::ROWS + at, vin ? vs + (long long)r * P.d_vh + c * 16 : P.V, vin);
+      }
+      const uint32_t meta = dst + 2 * S::ROWS + 16 * sub;
+      if (lane == 0) cp_async4(meta, P.Ks + blk);
+      if (lane == 1) cp_async4(meta + 4, P.Vs + blk);
+      if (lane == 2)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + 8), "r"(ok ? 1u : 0u) : "memory");
+    }
+  };
+
+  // the tile's rows: this thread holds rows g and (RH = 2) g + 8
+  uint32_t qa[KC * 4][RH * 2], ql[F32 ? KC * 4 : 1][RH * 2];
+  float qf[RH];
+  int limit[RH];    // last key that the row sees, -1: none
+  int lim_all = 0;  // every row that sees keys sees the keys up to here
+  int lim_any = -1; // no row sees keys past this
+  float m[RH], l[RH], z[RH][NT][2];
+  bool piece_starts = true;
+  int start_gi = 0;
+
+  auto begin_tile = [&]() {
+    const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
+    bool bad;
+    const Item it = item_of(P, cc.b, bad);
+    int lo = 0x7fffffff, hi = -1;
+#pragma unroll
+    for (int rh = 0; rh < RH; ++rh) {
+      const int r = rt * 16 + g + 8 * rh;
+      const int i = r / P.share;
+      const bool in = r < P.n_q * P.share && i < it.fresh;
+      limit[rh] = -1;
+      if (in) limit[rh] = P.causal_tail ? max(-1, it.total - it.fresh + i) : it.total - 1;
+      if (limit[rh] >= 0) lo = min(lo, limit[rh]);
+      hi = max(hi, limit[rh]);
+      m[rh] = -INFINITY;
+      l[rh] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) z[rh][n][0] = z[rh][n][1] = 0.f;
+      // the row's elements 64 i + 16 t + (0 .. 15)
+      const int head = kv * P.share + (r - i * P.share);
+      const long long at = (((long long)cc.b * P.h + head) * P.n_q + i) * P.d_h + 16 * t;
+      float q[KC][16];
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) q[k][e] = 0.f;
+        if (in && 64 * k + 16 * t < P.d_h) {
+          if constexpr (F32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(P.Q) + at + 64 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 u = __ldg(p + e);
+              q[k][4 * e] = u.x; q[k][4 * e + 1] = u.y; q[k][4 * e + 2] = u.z; q[k][4 * e + 3] = u.w;
+            }
+          } else {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.Q) + at + 64 * k);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 u = __ldg(p + e);
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                q[k][8 * e + 2 * f] = __uint_as_float(x[f] << 16);
+                q[k][8 * e + 2 * f + 1] = __uint_as_float(x[f] & 0xffff0000u);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(q[k][e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - E) for a largest element in [2^E, 2^(E + 1))
+      int E = (int)(__float_as_uint(top) >> 23) - 127;
+      E = E > 127 || top == 0.f ? 14 : max(E, -100);
+      const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+      qf[rh] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) q[k][e] *= up;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          qa[4 * k + f][2 * rh] = pack_half(q[k][4 * f], q[k][4 * f + 1]);
+          qa[4 * k + f][2 * rh + 1] = pack_half(q[k][4 * f + 2], q[k][4 * f + 3]);
+          if constexpr (F32) {
+            ql[4 * k + f][2 * rh] = rest_half(q[k][4 * f], q[k][4 * f + 1], qa[4 * k + f][2 * rh]);
+            ql[4 * k + f][2 * rh + 1] =
+                rest_half(q[k][4 * f + 2], q[k][4 * f + 3], qa[4 * k + f][2 * rh + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    lim_all = lo;
+    lim_any = hi;
+    piece_starts = false;
+    start_gi = cc.gi;
+  };
+
+  auto fold = [&](int stage) {
+    const uint32_t src = ring + stage * S::BYTES;
+#pragma unroll 1
+    for (int sub = 0; sub < S::SUBS; ++sub) {
+      const int kb = cc.gi * S::SK + 16 * sub;
+      if (kb > lim_any) break;
+      const uint4 meta = lds128(src + 2 * S::ROWS + 16 * sub);
+      if (!meta.z) continue;  // no such block
+      // scores
+      float s[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        float s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          const uint4 u = lds128(src + piece_at<D>(16 * sub + 8 * nt + g, t + 4 * k));
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const uint32_t b0 = e4m3_lo(x[f]), b1 = e4m3_hi(x[f]);
+            const uint32_t(&a)[RH * 2] = qa[4 * k + f];
+            mma_f16(s[nt], a[0], RH == 2 ? a[RH * 2 - 2] : 0u, a[1], RH == 2 ? a[RH * 2 - 1] : 0u, b0, b1);
+            if constexpr (F32) {
+              const uint32_t(&c)[RH * 2] = ql[4 * k + f];
+              mma_f16(s2, c[0], RH == 2 ? c[RH * 2 - 2] : 0u, c[1], RH == 2 ? c[RH * 2 - 1] : 0u, b0, b1);
+            }
+          }
+        }
+        if constexpr (F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] += s2[e];
+        }
+      }
+      // the group's own summary: weights against its maximum
+      const bool masked = kb + 15 > lim_all;
+      const float scale = __uint_as_float(meta.x) * P.cl2;
+      const float vscale = __uint_as_float(meta.y) * 6.103515625e-05f;  // 2^-14
+      uint32_t pa[2][2], pl[2][2];  // [row half][k half]
+      float alpha[RH], beta[RH];
+      bool raised = false;
+      pa[1][0] = pa[1][1] = pl[1][0] = pl[1][1] = 0u;
+#pragma unroll
+      for (int rh = 0; rh < RH; ++rh) {
+        const float f = scale * qf[rh];
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = s[e >> 1][2 * rh + (e & 1)] * f;
+          if (masked && kb + 8 * (e >> 1) + 2 * t + (e & 1) > limit[rh]) v[e] = -INFINITY;
+        }
+        float mg = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 1));
+        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 2));
+        const float mn = fmaxf(m[rh], mg);
+        const float base = mg == -INFINITY ? 0.f : mg;  // an empty group: every weight 0
+        alpha[rh] = mn == m[rh] ? 1.f : ex2_approx(m[rh] - mn);
+        beta[rh] = mg == mn ? 1.f : ex2_approx(mg - mn);
+        if (mg == -INFINITY) beta[rh] = 0.f;
+        raised |= alpha[rh] != 1.f;
+        m[rh] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = ex2_approx(v[e] - base);
+          sum += v[e];
+          v[e] *= 16384.f;
+        }
+        l[rh] = l[rh] * alpha[rh] + sum * beta[rh];
+        beta[rh] *= vscale;
+        pa[rh][0] = pack_half(v[0], v[1]);
+        pa[rh][1] = pack_half(v[2], v[3]);
+        if constexpr (F32) {
+          pl[rh][0] = rest_half(v[0], v[1], pa[rh][0]);
+          pl[rh][1] = rest_half(v[2], v[3], pa[rh][1]);
+        }
+      }
+      if (__any_sync(0xffffffffu, raised)) {
+#pragma unroll
+        for (int rh = 0; rh < RH; ++rh) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            z[rh][n][0] *= alpha[rh];
+            z[rh][n][1] *= alpha[rh];
+          }
+        }
+      }
+      // values: rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group
+      bool nan = false;
+      const int vr = 16 * sub + 2 * t;
+#pragma unroll
+      for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
+        constexpr int WORDS = D == 64 ? 2 : 4;
+        uint32_t x[4][WORDS];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = vr + (r & 1) + 8 * (r >> 1);
+          if constexpr (D == 64) {
+            const uint2 u = lds64(src + S::ROWS + piece_at<D>(row, g >> 1) + 8 * (g & 1));
+            x[r][0] = u.x; x[r][1] = u.y;
+          } else {
+            const uint4 u = lds128(src + S::ROWS + piece_at<D>(row, g + 8 * half));
+            x[r][0] = u.x; x[r][1] = u.y; x[r][2] = u.z; x[r][3] = u.w;
+          }
+          if (masked) {
+            // a NaN value must not reach the rows that do not see its key:
+            // it is taken out here and put back below
+#pragma unroll
+            for (int q = 0; q < WORDS; ++q) {
+              const uint32_t hit = ((x[r][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              nan |= hit != 0;
+              x[r][q] &= ~((hit >> 7) * 0xffu);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < WORDS; ++q) {
+#pragma unroll
+          for (int hq = 0; hq < 2; ++hq) {
+            const uint32_t sel = hq ? 0x7362u : 0x5140u;
+            const uint32_t u0 = __byte_perm(x[0][q], x[1][q], sel);
+            const uint32_t u1 = __byte_perm(x[2][q], x[3][q], sel);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int n = half * 16 + q * 4 + hq * 2 + o;
+              const uint32_t b0 = o ? e4m3_hi(u0) : e4m3_lo(u0);
+              const uint32_t b1 = o ? e4m3_hi(u1) : e4m3_lo(u1);
+              float a[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(a, pa[0][0], pa[1][0], pa[0][1], pa[1][1], b0, b1);
+              if constexpr (F32) mma_f16(a, pl[0][0], pl[1][0], pl[0][1], pl[1][1], b0, b1);
+#pragma unroll
+              for (int rh = 0; rh < RH; ++rh) {
+                z[rh][n][0] = fmaf(beta[rh], a[2 * rh], z[rh][n][0]);
+                z[rh][n][1] = fmaf(beta[rh], a[2 * rh + 1], z[rh][n][1]);
+              }
+            }
+          }
+        }
+      }
+      if (masked && __any_sync(0xffffffffu, nan)) {
+        for (int key = 0; key < 16; ++key) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int d = D == 64 ? 8 * (2 * t + e) + n : (n & 16) * 8 + 16 * (2 * t + e) + (n & 15);
+              const uint32_t v = lds8(src + S::ROWS + piece_at<D>(16 * sub + key, d >> 4) + (d & 15));
+              if ((v & 0x7f) != 0x7f) continue;
+#pragma unroll
+              for (int rh = 0; rh < RH; ++rh)
+                if (kb + key <= limit[rh]) z[rh][n][e] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+      }
+    }
+  };
+
+  // The summary of the keys [start_gi, cc.gi] of the tile: z / l when these
+  // are all, else to the workspace.
+  auto end_piece = [&]() {
+    const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
+    const bool whole = start_gi == 0 && cc.gi == cc.ng - 1;
+    constexpr int COLS = D / 4;  // consecutive columns that this thread holds
+#pragma unroll
+    for (int rh = 0; rh < RH; ++rh) {
+      float sum = l[rh];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int r = rt * 16 + g + 8 * rh;
+      if (r >= P.n_q * P.share) continue;
+      const float inv = whole ? (limit[rh] < 0 ? 0.f : 1.f / sum) : 1.f;
+      const bool empty = whole && (limit[rh] < 0 || sum == 0.f);
+      const int i = r / P.share, head = kv * P.share + (r - i * P.share);
+      const long long zat = ((long long)cc.b * P.n_q + i) * P.h * P.d_vh + (long long)head * P.d_vh;
+      const long long slot = 2ll * w + (start_gi == 0 ? 1 : 0);
+      const long long at = slot * P.slot_rows + (g + 8 * rh);
+      float* pz = P.part + 2ll * 2 * P.warps * P.slot_rows + at * P.d_vh;
+      if (!whole && t == 0) {
+        P.part[2 * at] = m[rh];
+        P.part[2 * at + 1] = sum;
+      }
+#pragma unroll
+      for (int c = 0; c < COLS; c += 8) {
+        // columns of this thread: half, e and n as in fold
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          int n, e;
+          if constexpr (D == 64) {
+            n = (c + k) & 7;
+            e = (c + k) >> 3;
+          } else {
+            n = ((c + k) & 15) + ((c + k) >> 5) * 16;
+            e = ((c + k) >> 4) & 1;
+          }
+          v[k] = empty ? 0.f : z[rh][n][e] * inv;
+        }
+        const int col = D == 64 ? 16 * t + c : (c >> 5) * 128 + 32 * t + (c & 31);
+        if (col >= P.d_vh) continue;
+        if (!whole) {
+          *reinterpret_cast<float4*>(pz + col) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(pz + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else if constexpr (F32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(P.Z) + zat + col);
+          o[0] = make_float4(v[0], v[1], v[2], v[3]);
+          o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.Z) + zat + col) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        }
+      }
+    }
+  };
+
+  // fill the ring
+#pragma unroll
+  for (int k = 0; k < S::N - 1; ++k) {
+    if (load_left > 0) {
+      issue(k);
+      advance(lc);
+      --load_left;
+    }
+    cp_async_commit();
+  }
+  int stage = 0;
+  for (; left > 0; --left) {
+    cp_async_wait<S::N - 2>();
+    __syncwarp();  // the stage is filled, and every lane has left the one before
+    if (load_left > 0) {
+      issue(stage == 0 ? S::N - 1 : stage - 1);
+      advance(lc);
+      --load_left;
+    }
+    cp_async_commit();
+    if (piece_starts) begin_tile();
+    fold(stage);
+    if (cc.gi == cc.ng - 1 || left == 1) {
+      end_piece();
+      piece_starts = true;
+    }
+    advance(cc);
+    stage = stage == S::N - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+}
+
+// One output row per CTA: zeros where it sees no key, else the merge of its
+// tile's pieces in order, unless a single warp had the tile whole and wrote it.
+template <int D, typename T>
+__global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_constant__ CacheAttnParams P) {
+  constexpr int CT = D / 4;              // threads across the columns, 4 each
+  constexpr int PG = CM_THREADS / CT;    // pieces at a time
+  __shared__ float sm[PG][2];
+  __shared__ __align__(16) float sz[PG][D];
+  grid_dep_wait();
+  const int head = blockIdx.x % P.h;
+  const long long bi = blockIdx.x / P.h;
+  const int i = (int)(bi % P.n_q), b = (int)(bi / P.n_q);
+  const int kv = head / P.share, r = i * P.share + head % P.share;
+  const int pr = kv * P.tiles + r / 16, row = r % 16;
+  const int unit = P.h_kv * P.tiles;
+  const int f0 = P.first[b], ng = P.first[b + 1] - f0;
+  const long long G = (long long)P.first[P.B] * unit;
+  const int col = threadIdx.x % CT * 4, pg = threadIdx.x / CT;
+  T* out = static_cast<T*>(P.Z) + (bi * P.h + head) * P.d_vh + col;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  bool bad;
+  const Item it = item_of(P, b, bad);
+  if (ng > 0) {
+    const long long a = (long long)f0 * unit + (long long)pr * ng;
+    const int w0 = (int)(((a + 1) * P.warps - 1) / G), w1 = (int)(((a + ng) * P.warps - 1) / G);
+    if (w0 == w1) return;
+    const float* ml = P.part;
+    const float* pz = P.part + 2ll * 2 * P.warps * P.slot_rows;
+    for (int w = w0 + pg; w <= w1; w += PG) {
+      const long long s0 = w * G / P.warps;
+      if (s0 == (w + 1) * G / P.warps) continue;  // a warp without work
+      const long long at = (2ll * w + (s0 <= a ? 1 : 0)) * P.slot_rows + row;
+      const float mw = ml[2 * at], lw = ml[2 * at + 1];
+      if (mw == -INFINITY && lw == 0.f) continue;  // the empty summary
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (col < P.d_vh) v = *reinterpret_cast<const float4*>(pz + at * P.d_vh + col);
+      const float mn = fmaxf(m, mw);
+      const float x = m == mn ? 1.f : exp2f(m - mn), y = mw == mn ? 1.f : exp2f(mw - mn);
+      acc.x = acc.x * x + v.x * y;
+      acc.y = acc.y * x + v.y * y;
+      acc.z = acc.z * x + v.z * y;
+      acc.w = acc.w * x + v.w * y;
+      l = l * x + lw * y;
+      m = mn;
+    }
+  }
+  if (threadIdx.x % CT == 0) {
+    sm[pg][0] = m;
+    sm[pg][1] = l;
+  }
+  *reinterpret_cast<float4*>(&sz[pg][col]) = acc;
+  __syncthreads();
+  if (pg != 0 || col >= P.d_vh) return;
+#pragma unroll
+  for (int k = 1; k < PG; ++k) {
+    const float mw = sm[k][0];
+    if (mw == -INFINITY && sm[k][1] == 0.f) continue;
+    const float mn = fmaxf(m, mw);
+    const float x = m == mn ? 1.f : exp2f(m - mn), y = mw == mn ? 1.f : exp2f(mw - mn);
+    acc.x = acc.x * x + sz[k][col] * y;
+    acc.y = acc.y * x + sz[k][col + 1] * y;
+    acc.z = acc.z * x + sz[k][col + 2] * y;
+    acc.w = acc.w * x + sz[k][col + 3] * y;
+    l = l * x + sm[k][1] * y;
+    m = mn;
+  }
+  const bool none = i >= it.fresh || l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(out) =
+        none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint2*>(out) =
+        none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+}
+
+template <int D, int RH, bool F32>
+mha_status launch(CacheAttnParams& P, cudaStream_t s) {
+  auto* kernel = cache_attention_kernel<D, RH, F32>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), Stage<D>::SMEM)) return MHA_ERR_CUDA;
+  const int ctas = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
+  P.warps = ctas * CA_WARPS;
+  cudaError_t e = launch_dependent(kernel, dim3(ctas), dim3(CA_THREADS), Stage<D>::SMEM, s, P);
+  if (e == cudaSuccess) {
+    using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    e = launch_dependent(cache_merge_kernel<D, T>, dim3((unsigned)((long long)P.B * P.n_q * P.h)),
+                         dim3(CM_THREADS), 0, s, P);
+  }
+  count_launch(2);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+template <int D>
+mha_status launch_rows(CacheAttnParams& P, mha_dtype dt, cudaStream_t s) {
+  const bool two = P.n_q * P.share > 8;
+  if (dt == MHA_DTYPE_F32) return two ? launch<D, 2, true>(P, s) : launch<D, 1, true>(P, s);
+  return two ? launch<D, 2, false>(P, s) : launch<D, 1, false>(P, s);
+}
+
+}  // namespace
+
+size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_vh) {
+  const long long rows = (long long)n_q * (h / h_kv);
+  return CA_HEADER + (size_t)2 * CA_MAX_CTAS * CA_WARPS * (rows < 16 ? rows : 16) *
+                         (2 + (size_t)d_vh) * sizeof(float);
+}
+
+mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s) {
+  CacheAttnParams P{};
+  P.Q = a.Q;
+  P.K = static_cast<const uint8_t*>(a.K_cache);
+  P.V = static_cast<const uint8_t*>(a.V_cache);
+  P.Ks = a.K_scale;
+  P.Vs = a.V_scale;
+  P.table = a.block_table;
+  P.total = a.total_len;
+  P.fresh = a.new_len;
+  P.Z = a.Z;
+  P.first = static_cast<int32_t*>(a.workspace);
+  P.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + CA_HEADER);
+  P.err = a.err;
+  P.B = a.B;
+  P.n_q = a.n_q;
+  P.h = a.h;
+  P.h_kv = a.h_kv;
+  P.share = a.h / a.h_kv;
+  P.d_h = a.d_h;
+  P.d_vh = a.d_vh;
+  P.n_blocks = a.n_blocks;
+  P.bt = a.bt;
+  P.max_blocks = a.max_blocks;
+  const int rows = a.n_q * P.share;
+  P.tiles = (rows + 15) / 16;
+  P.slot_rows = rows < 16 ? rows : 16;
+  P.causal_tail = a.causal_tail;
+  P.cl2 = a.c * 1.4426950408889634f;
+  const int d = a.d_h > a.d_vh ? a.d_h : a.d_vh;
+  if (d <= 64) return launch_rows<64>(P, dt, s);
+  if (d <= 128) return launch_rows<128>(P, dt, s);
+  return launch_rows<256>(P, dt, s);
+}
+
+}  // namespace mha

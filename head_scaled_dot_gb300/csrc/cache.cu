@@ -1,0 +1,401 @@
+// cache.cu - the key/value cache in blocks of tokens: blocks and slots for new
+// rows (reserve, release) and appending rows in 8 bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+
+namespace mha {
+namespace {
+
+__device__ __forceinline__ void report(int32_t* err, int code) {
+  if (err) atomicCAS(err, 0, code);
+}
+
+// ---------------------------------------------------------------------------
+// Blocks and slots
+// ---------------------------------------------------------------------------
+//
+// A sequence of L cached rows holds ceil(L / bt) blocks; a new rows make it
+// need(b) = ceil((L + a) / bt) - ceil(L / bt) more. With P the inclusive sum
+// of need over the sequences in order, sequence b is admitted when need(b) is
+// 0 or P(b) <= n_free, and takes the free blocks P(b) - need(b) ... P(b) - 1
+// from the top of the free stack. The sum, not an atomic counter, hands out
+// the blocks, so the same lengths always give the same table.
+//
+// The kernel is latency (a few loads and one scan over at most 1024 lengths)
+// plus 8 bytes per slot: every CTA repeats the scan and then writes its share
+// of the table and of the slots, so one launch does and no CTA waits for
+// another.
+
+constexpr int RES_THREADS = 256;
+constexpr int RES_ITEMS = MHA_MAX_PADDED_BATCH / RES_THREADS;  // sequences per thread
+
+struct ReserveParams {
+  const int32_t* cached_len;
+  const int32_t* new_len;     // release: the sequences' flags
+  int32_t* free_blocks;       // written by release only
+  const int32_t* n_free;
+  int32_t* block_table;
+  int64_t* slot_map;
+  int32_t* total_len;
+  int32_t* n_free_out;
+  int32_t* err;
+  int B, n, capacity, max_blocks, bt;
+};
+
+// Inclusive sum of one int per thread over the CTA.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  return v + before;
+}
+
+__global__ void __launch_bounds__(RES_THREADS) reserve_kernel(const __grid_constant__ ReserveParams P) {
+  __shared__ int warp_sums[RES_THREADS / 32];
+  __shared__ int s_len[MHA_MAX_PADDED_BATCH];    // rows before
+  __shared__ int s_new[MHA_MAX_PADDED_BATCH];    // rows admitted
+  __shared__ int s_first[MHA_MAX_PADDED_BATCH];  // place of its first new block on the stack
+  __shared__ int s_used;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (threadIdx.x == 0) s_used = 0;
+
+  int n_free = __ldg(P.n_free);
+  bool bad = n_free < 0 || n_free > P.capacity;
+  n_free = min(max(n_free, 0), P.capacity);
+  int len[RES_ITEMS], add[RES_ITEMS], need[RES_ITEMS], sum = 0;
+#pragma unroll
+  for (int k = 0; k < RES_ITEMS; ++k) {
+    const int b = threadIdx.x * RES_ITEMS + k;
+    len[k] = add[k] = need[k] = 0;
+    if (b < P.B) {
+      len[k] = __ldg(P.cached_len + b);
+      add[k] = __ldg(P.new_len + b);
+      const long long rows = (long long)len[k] + add[k];
+      if (len[k] < 0 || add[k] < 0 || add[k] > P.n || rows > (long long)P.max_blocks * P.bt) {
+        bad = true;
+        add[k] = -1;  // refused
+      } else {
+        need[k] = (int)((rows + P.bt - 1) / P.bt) - (int)(((long long)len[k] + P.bt - 1) / P.bt);
+      }
+    }
+    sum += need[k];
+  }
+  const int upto = block_scan(sum, warp_sums);  // its __syncthreads also orders s_used
+  int last = upto - sum, used = 0;
+  bool full = false;
+#pragma unroll
+  for (int k = 0; k < RES_ITEMS; ++k) {
+    const int b = threadIdx.x * RES_ITEMS + k;
+    last += need[k];
+    const bool fits = add[k] >= 0 && (need[k] == 0 || last <= n_free);
+    if (fits && need[k] > 0) used = last;
+    full |= add[k] >= 0 && !fits;
+    if (b < P.B) {
+      s_len[b] = len[k];
+      s_new[b] = fits ? add[k] : 0;
+      s_first[b] = n_free - 1 - (last - need[k]);
+    }
+  }
+  if (used) atomicMax(&s_used, used);
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+    if (bad) report(P.err, MHA_ERR_INVALID_ARG);
+    if (full) report(P.err, MHA_ERR_CACHE_FULL);
+    if (threadIdx.x == 0) *P.n_free_out = n_free - s_used;
+    for (int b = threadIdx.x; b < P.B; b += RES_THREADS) P.total_len[b] = s_len[b] + s_new[b];
+  }
+  // new entries of the block table
+  for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+    const int have = (int)(((long long)s_len[b] + P.bt - 1) / P.bt);
+    const int want = (int)(((long long)s_len[b] + s_new[b] + P.bt - 1) / P.bt);
+    for (int j = have + threadIdx.x; j < want; j += RES_THREADS)
+      P.block_table[(long long)b * P.max_blocks + j] = __ldg(P.free_blocks + s_first[b] - (j - have));
+  }
+  // slots: a new block's number comes from the stack, the last old block's
+  // from the table (whose entries before `have` this kernel does not write)
+  const long long slots = (long long)P.B * P.n;
+  for (long long e = (long long)blockIdx.x * RES_THREADS + threadIdx.x; e < slots;
+       e += (long long)gridDim.x * RES_THREADS) {
+    const int b = (int)(e / P.n), i = (int)(e - (long long)b * P.n);
+    int64_t slot = -1;
+    if (i < s_new[b]) {
+      const int pos = s_len[b] + i, j = pos / P.bt;
+      const int have = (int)(((long long)s_len[b] + P.bt - 1) / P.bt);
+      const int id = j < have ? __ldg(P.block_table + (long long)b * P.max_blocks + j)
+                              : __ldg(P.free_blocks + s_first[b] - (j - have));
+      if (id < 0)
+        report(P.err, MHA_ERR_INVALID_ARG);
+      else
+        slot = (int64_t)id * P.bt + (pos - j * P.bt);
+    }
+    P.slot_map[e] = slot;
+  }
+}
+
+// The blocks of the flagged sequences go back on top of the free stack, in
+// the sequences' order.
+__global__ void __launch_bounds__(RES_THREADS) release_kernel(const __grid_constant__ ReserveParams P) {
+  __shared__ int warp_sums[RES_THREADS / 32];
+  __shared__ int s_have[MHA_MAX_PADDED_BATCH], s_first[MHA_MAX_PADDED_BATCH];
+  __shared__ int s_used;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (threadIdx.x == 0) s_used = 0;
+  int n_free = __ldg(P.n_free);
+  bool bad = n_free < 0 || n_free > P.capacity;
+  n_free = min(max(n_free, 0), P.capacity);
+  int len[RES_ITEMS], have[RES_ITEMS], sum = 0;
+#pragma unroll
+  for (int k = 0; k < RES_ITEMS; ++k) {
+    const int b = threadIdx.x * RES_ITEMS + k;
+    len[k] = have[k] = 0;
+    if (b < P.B) {
+      len[k] = __ldg(P.cached_len + b);
+      if (__ldg(P.new_len + b) != 0) {
+        const long long blocks = ((long long)len[k] + P.bt - 1) / P.bt;
+        if (len[k] < 0 || blocks > P.max_blocks) bad = true;
+        else have[k] = (int)blocks;
+      }
+    }
+    sum += have[k];
+  }
+  int last = block_scan(sum, warp_sums) - sum, used = 0;
+#pragma unroll
+  for (int k = 0; k < RES_ITEMS; ++k) {
+    const int b = threadIdx.x * RES_ITEMS + k;
+    last += have[k];
+    const bool fits = have[k] == 0 || last <= P.capacity - n_free;
+    if (!fits) bad = true;  // more blocks than the pool has: a table or length is wrong
+    if (fits && have[k] > 0) used = last;
+    if (b < P.B) {
+      s_have[b] = fits ? have[k] : 0;
+      s_first[b] = n_free + last - have[k];
+      if (blockIdx.x == 0) {
+        const bool gone = __ldg(P.new_len + b) != 0 && len[k] >= 0 && fits &&
+                          ((long long)len[k] + P.bt - 1) / P.bt <= P.max_blocks;
+        P.total_len[b] = gone ? 0 : len[k];
+      }
+    }
+  }
+  if (used) atomicMax(&s_used, used);
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    if (bad) report(P.err, MHA_ERR_INVALID_ARG);
+    if (threadIdx.x == 0) *P.n_free_out = n_free + s_used;
+  }
+  for (int b = blockIdx.x; b < P.B; b += gridDim.x)
+    for (int j = threadIdx.x; j < s_have[b]; j += RES_THREADS)
+      P.free_blocks[s_first[b] + j] = __ldg(P.block_table + (long long)b * P.max_blocks + j);
+}
+
+// ---------------------------------------------------------------------------
+// Append in 8 bits
+// ---------------------------------------------------------------------------
+//
+// A block of a head keeps its rows as e4m3 numbers times one scale. The scale
+// is the smallest power of two s with max |x| / s <= 448 over the rows that
+// the block holds, and it only grows while the block holds rows. e4m3 is a
+// floating-point format, so a power of two loses no precision against
+// max / 448 (only up to one of the 18 binary orders between its largest and
+// smallest number), and it makes x / s exact: each value is rounded once.
+// Where new rows raise a block's scale, its older rows are multiplied by the
+// exact ratio of the scales and rounded again, which changes only those that
+// fall below the smallest normal number, 2^-6.
+
+constexpr int APP_THREADS = 128;
+
+struct AppendParams {
+  const void* x[2];   // K, V: (B, h, n, d)
+  uint8_t* cache[2];  // (n_blocks, h, bt, d)
+  float* scale[2];    // (n_blocks, h)
+  int d[2];
+  const int64_t* slot_map;
+  int32_t* err;
+  int B, h, n, bt, n_blocks;
+};
+
+__device__ __forceinline__ float block_max(float v, float* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = s[0];
+#pragma unroll
+  for (int w = 1; w < APP_THREADS / 32; ++w) v = fmaxf(v, s[w]);
+  return v;
+}
+
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Two values as e4m3 (round to nearest even, beyond 448 to 448, NaN to NaN).
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint2 pack_e4m3x8(const float (&v)[8]) {
+  return make_uint2(pack_e4m3x2(v[0], v[1]) | pack_e4m3x2(v[2], v[3]) << 16,
+                    pack_e4m3x2(v[4], v[5]) | pack_e4m3x2(v[6], v[7]) << 16);
+}
+__device__ __forceinline__ void unpack_e4m3x8(uint2 u, float (&v)[8]) {
+  const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// The smallest power of two s, at least 2^-126, with amax / s <= 448 = 1.75 * 2^8.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u);  // biased exponent of s
+  e = max(e, 1);  // also for amax = 0 and denormals
+  return __uint_as_float((uint32_t)e << 23);
+}
+
+// One CTA: the rows of one batch item that lie in one block of one head, of K
+// or of V. grid (parts, h, 2 B).
+template <typename T>
+__global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_constant__ AppendParams P) {
+  __shared__ float red[APP_THREADS / 32];
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int which = blockIdx.z & 1, b = blockIdx.z >> 1, head = blockIdx.y;
+  const int64_t* slots = P.slot_map + (long long)b * P.n;
+  const int64_t first = __ldg(slots);
+  if (first < 0) return;  // no new rows
+  const int off = (int)(first % P.bt);
+  const int row0 = blockIdx.x == 0 ? 0 : blockIdx.x * P.bt - off;  // first row of the part
+  if (row0 >= P.n) return;
+  const int64_t slot0 = __ldg(slots + row0);
+  if (slot0 < 0) return;  // past the item's last row
+  const int64_t block = slot0 / P.bt;
+  const int kept = blockIdx.x == 0 ? off : 0;  // rows that the block holds already
+  const int rows = min(P.bt - kept, P.n - row0);
+  if (block >= P.n_blocks || slot0 != block * P.bt + kept) {
+    if (threadIdx.x == 0) report(P.err, MHA_ERR_INVALID_ARG);
+    return;
+  }
+  const int d = P.d[which], vecs = d / 8;
+  const T* x = static_cast<const T*>(P.x[which]) + (((long long)b * P.h + head) * P.n + row0) * d;
+  uint8_t* out = P.cache[which] + (block * P.h + head) * (long long)P.bt * d;
+  float* scale = P.scale[which] + block * P.h + head;
+
+  float amax = 0.f;
+  bool odd = false;
+  for (int e = threadIdx.x; e < rows * vecs; e += APP_THREADS) {
+    const int r = e / vecs;
+    const int64_t slot = __ldg(slots + row0 + r);
+    if (slot != slot0 + r) {
+      odd |= slot >= 0;
+      continue;
+    }
+    float v[8];
+    load8(x + (long long)e * 8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(v[i]);
+      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // finite values only
+    }
+  }
+  if (odd) report(P.err, MHA_ERR_INVALID_ARG);
+  const float before = kept ? *scale : 0.f;
+  amax = block_max(amax, red);  // its barrier: every thread has read the old scale
+  float s = pow2_scale(amax);
+  if (kept) s = fmaxf(s, before);
+  if (threadIdx.x == 0) *scale = s;
+  if (kept && s > before) {
+    const float ratio = before / s;
+    for (int e = threadIdx.x; e < kept * vecs; e += APP_THREADS) {
+      uint2* p = reinterpret_cast<uint2*>(out) + e;
+      float v[8];
+      unpack_e4m3x8(*p, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= ratio;
+      *p = pack_e4m3x8(v);
+    }
+  }
+  for (int e = threadIdx.x; e < rows * vecs; e += APP_THREADS) {
+    const int r = e / vecs;
+    if (__ldg(slots + row0 + r) != slot0 + r) continue;
+    float v[8];
+    load8(x + (long long)e * 8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
+    reinterpret_cast<uint2*>(out + (long long)kept * d)[e] = pack_e4m3x8(v);
+  }
+}
+
+}  // namespace
+
+mha_status cache_reserve(const ReserveArgs& a, bool release, cudaStream_t s) {
+  ReserveParams P{a.cached_len, a.new_len,   a.free_blocks, a.n_free, a.block_table,
+                  a.slot_map,   a.total_len, a.n_free_out,  a.err,    a.B,
+                  a.n,          a.capacity,  a.max_blocks,  a.bt};
+  cudaError_t e;
+  if (release) {
+    const int grid = a.B < num_sms() ? a.B : num_sms();
+    e = launch_dependent(release_kernel, dim3(grid), dim3(RES_THREADS), 0, s, P);
+  } else {
+    // about 8 slots per thread, at most two CTAs per SM: each repeats the scan
+    long long grid = ((long long)a.B * a.n + 8 * RES_THREADS - 1) / (8 * RES_THREADS);
+    if (grid > 2 * num_sms()) grid = 2 * num_sms();
+    e = launch_dependent(reserve_kernel, dim3((unsigned)grid), dim3(RES_THREADS), 0, s, P);
+  }
+  count_launch();
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+mha_status cache_append(const AppendArgs& a, mha_dtype dt, cudaStream_t s) {
+  AppendParams P{{a.K, a.V},
+                 {static_cast<uint8_t*>(a.K_cache), static_cast<uint8_t*>(a.V_cache)},
+                 {a.K_scale, a.V_scale},
+                 {a.d_h, a.d_vh},
+                 a.slot_map,
+                 a.err,
+                 a.B,
+                 a.h,
+                 a.n,
+                 a.bt,
+                 a.n_blocks};
+  const int parts = (int)(((long long)a.bt - 1 + a.n - 1) / a.bt) + 1;
+  const dim3 grid(parts, a.h, 2 * a.B);
+  const cudaError_t e =
+      dt == MHA_DTYPE_F32
+          ? launch_dependent(append_kernel<float>, grid, dim3(APP_THREADS), 0, s, P)
+          : launch_dependent(append_kernel<__nv_bfloat16>, grid, dim3(APP_THREADS), 0, s, P);
+  count_launch();
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+}  // namespace mha

@@ -96,6 +96,72 @@ struct DecodeArgs {
 size_t decode_workspace_bytes(int B, int n_q, int n_k, int h, int d_vh);
 mha_status attention_decode(const DecodeArgs& a, mha_dtype dt, cudaStream_t s);
 
+// Rotary positions with several axes on head-split Q (B,h,T,d) and, unless
+// null, K (B,h_kv,T,d) (rotary.cu). positions (n_axes,B,T), steps one per pair;
+// sections: host, pairs of each axis.
+struct RotaryArgs {
+  const void* Q;
+  const void* K;
+  void* Q_out;
+  void* K_out;
+  const int32_t* positions;
+  const uint64_t* steps;
+  const int32_t* sections;
+  int n_axes, B, T, h, h_kv, d;
+  int interleaved, inverse;
+};
+mha_status rotary(const RotaryArgs& a, mha_dtype dt, cudaStream_t s);
+
+// Blocks and slots for new rows, or blocks given back (cache.cu); for release
+// new_len holds the sequences' flags and slot_map is not used.
+struct ReserveArgs {
+  const int32_t* cached_len;
+  const int32_t* new_len;
+  int32_t* free_blocks;
+  const int32_t* n_free;
+  int32_t* block_table;
+  int64_t* slot_map;
+  int32_t* total_len;
+  int32_t* n_free_out;
+  int32_t* err;
+  int B, n, capacity, max_blocks, bt;
+};
+mha_status cache_reserve(const ReserveArgs& a, bool release, cudaStream_t s);
+
+// Rows K (B,h,n,d_h), V (B,h,n,d_vh) into an 8-bit cache (cache.cu).
+struct AppendArgs {
+  const void* K;
+  const void* V;
+  const int64_t* slot_map;
+  void* K_cache;
+  void* V_cache;
+  float* K_scale;
+  float* V_scale;
+  int32_t* err;
+  int B, n, h, d_h, d_vh, n_blocks, bt;
+};
+mha_status cache_append(const AppendArgs& a, mha_dtype dt, cudaStream_t s);
+
+// Attention over an 8-bit cache (attn_cache.cu).
+struct CacheAttnArgs {
+  const void* Q;
+  const void* K_cache;
+  const void* V_cache;
+  const float* K_scale;
+  const float* V_scale;
+  const int32_t* block_table;
+  const int32_t* total_len;
+  const int32_t* new_len;  // or null: n_q everywhere
+  void* Z;
+  void* workspace;
+  int32_t* err;
+  int B, n_q, h, h_kv, d_h, d_vh, n_blocks, bt, max_blocks;
+  int causal_tail;
+  float c;
+};
+size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_vh);
+mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s);
+
 // Raises the dynamic shared-memory limit of `kernel` to `bytes` on the
 // current device, once per (device, kernel): the attribute belongs to the
 // device, not to the process. Thread-safe; false on a CUDA error.

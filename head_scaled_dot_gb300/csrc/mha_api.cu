@@ -284,6 +284,28 @@ mha_status run_out(const void* Z, const void* W_O, void* Y, int B, int n_q, int 
   return gemm_tc(&p, 1, &sel, err, s);
 }
 
+// The 8-bit cache: blocks of a multiple of 16 rows of a multiple of 16 bytes.
+bool cache_shape_ok(int d_h, int d_vh, int block_tokens) {
+  return d_h % 16 == 0 && d_vh % 16 == 0 && d_h <= MAX_HEAD_DIM && d_vh <= MAX_HEAD_DIM &&
+         block_tokens % 16 == 0 && block_tokens <= MHA_MAX_BLOCK_TOKENS;
+}
+
+// The block pool of mha_cache_reserve and mha_cache_release.
+mha_status check_pool(const ReserveArgs& a, bool release) {
+  if (!a.cached_len || !a.new_len || !a.free_blocks || !a.n_free || !a.block_table ||
+      !a.total_len || !a.n_free_out)
+    return MHA_ERR_INVALID_ARG;
+  if (a.B <= 0 || a.capacity <= 0 || a.max_blocks <= 0 || a.bt <= 0) return MHA_ERR_INVALID_ARG;
+  if (!release && (!a.slot_map || a.n <= 0)) return MHA_ERR_INVALID_ARG;
+  // every thread block reads the old state: the new one has its own place
+  if (a.n_free_out == a.n_free || a.total_len == a.cached_len || a.total_len == a.new_len)
+    return MHA_ERR_INVALID_ARG;
+  if (a.B > MHA_MAX_PADDED_BATCH || a.bt > MHA_MAX_BLOCK_TOKENS ||
+      !fits(a.max_blocks, a.bt, 1))
+    return MHA_ERR_UNSUPPORTED;
+  return MHA_OK;
+}
+
 // Split over the keys of one attention call: 1 none, 0 automatic within the
 // scratch, n > 1 n ranges; ws: device scratch (or null); zeroed: its counters
 // were zeroed on the stream by the caller.
@@ -581,6 +603,135 @@ mha_status mha_attention_decode(const void* Q, const void* K, const void* V, voi
   return attention_decode(a, dt, static_cast<cudaStream_t>(stream));
 }
 
+mha_status mha_rotary_steps(const int32_t* sections, int n_axes, double base, int per_axis,
+                            uint64_t* steps) {
+  if (!sections || !steps || n_axes <= 0 || !(base > 0.0) || !isfinite(base))
+    return MHA_ERR_INVALID_ARG;
+  if (n_axes > MHA_MAX_ROTARY_AXES) return MHA_ERR_UNSUPPORTED;
+  int pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0) return MHA_ERR_INVALID_ARG;
+    if (sections[a] > MAX_HEAD_DIM / 2 - pairs) return MHA_ERR_UNSUPPORTED;
+    pairs += sections[a];
+  }
+  if (pairs == 0) return MHA_ERR_INVALID_ARG;
+  int i = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    for (int j = 0; j < sections[a]; ++j, ++i) {
+      const double x = per_axis ? (double)j / sections[a] : (double)i / pairs;
+      // radians per position -> fraction of a turn per position, mod 1, times 2^64
+      double turn = pow(base, -x) * 0.15915494309189533577;
+      turn -= floor(turn);
+      steps[i] = turn < 1.0 ? (uint64_t)ldexp(turn, 64) : 0;
+    }
+  }
+  return MHA_OK;
+}
+
+mha_status mha_rotary(const void* Q, const void* K, const int32_t* positions,
+                      const uint64_t* steps, const int32_t* sections, int n_axes, void* Q_out,
+                      void* K_out, int B, int T, int h, int h_kv, int d, int interleaved,
+                      int inverse, mha_dtype dt, void* stream) {
+  if (!Q || !Q_out || !positions || !steps || !sections || (K != nullptr) != (K_out != nullptr))
+    return MHA_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || h <= 0 || d <= 0 || n_axes <= 0 || (K && h_kv <= 0) || !dtype_ok(dt))
+    return MHA_ERR_INVALID_ARG;
+  if (n_axes > MHA_MAX_ROTARY_AXES || d > MAX_HEAD_DIM || d % 2) return MHA_ERR_UNSUPPORTED;
+  int pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0 || sections[a] > d / 2 - pairs) return MHA_ERR_INVALID_ARG;
+    pairs += sections[a];
+  }
+  if (pairs == 0) return MHA_ERR_INVALID_ARG;
+  if (!fits(B, T, 1) || !fits((long long)h + (K ? h_kv : 0), 1, 1) ||
+      h + (long long)(K ? h_kv : 0) > 65535)
+    return MHA_ERR_UNSUPPORTED;
+  if (!aligned16(Q) || !aligned16(Q_out) || !aligned16(K) || !aligned16(K_out))
+    return MHA_ERR_UNSUPPORTED;
+  RotaryArgs a{Q, K, Q_out, K_out, positions, steps, sections, n_axes, B, T, h, h_kv, d,
+               interleaved ? 1 : 0, inverse ? 1 : 0};
+  return rotary(a, dt, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_cache_reserve(const int32_t* cached_len, const int32_t* new_len,
+                             const int32_t* free_blocks, const int32_t* n_free,
+                             int32_t* block_table, int64_t* slot_map, int32_t* total_len,
+                             int32_t* n_free_out, int B, int n, int n_blocks, int max_blocks,
+                             int block_tokens, int32_t* dev_error, void* stream) {
+  ReserveArgs a{cached_len, new_len, const_cast<int32_t*>(free_blocks), n_free, block_table,
+                slot_map, total_len, n_free_out, dev_error, B, n, n_blocks, max_blocks,
+                block_tokens};
+  const mha_status st = check_pool(a, false);
+  if (st != MHA_OK) return st;
+  return cache_reserve(a, false, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_cache_release(const int32_t* cached_len, const int32_t* finished,
+                             int32_t* free_blocks, const int32_t* n_free,
+                             const int32_t* block_table, int32_t* total_len,
+                             int32_t* n_free_out, int B, int n_blocks, int max_blocks,
+                             int block_tokens, int32_t* dev_error, void* stream) {
+  ReserveArgs a{cached_len, finished, free_blocks, n_free, const_cast<int32_t*>(block_table),
+                nullptr, total_len, n_free_out, dev_error, B, 0, n_blocks, max_blocks,
+                block_tokens};
+  const mha_status st = check_pool(a, true);
+  if (st != MHA_OK) return st;
+  return cache_reserve(a, true, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_cache_append(const void* K, const void* V, const int64_t* slot_map, void* K_cache,
+                            void* V_cache, float* K_scale, float* V_scale, int B, int n, int h,
+                            int d_h, int d_vh, int n_blocks, int block_tokens, mha_dtype dt,
+                            int32_t* dev_error, void* stream) {
+  if (!K || !V || !slot_map || !K_cache || !V_cache || !K_scale || !V_scale)
+    return MHA_ERR_INVALID_ARG;
+  if (B <= 0 || n <= 0 || h <= 0 || d_h <= 0 || d_vh <= 0 || n_blocks <= 0 || block_tokens <= 0 ||
+      !dtype_ok(dt))
+    return MHA_ERR_INVALID_ARG;
+  if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > 32767 || h > 65535)
+    return MHA_ERR_UNSUPPORTED;
+  if (!aligned16(K) || !aligned16(V) || !aligned16(K_cache) || !aligned16(V_cache))
+    return MHA_ERR_UNSUPPORTED;
+  AppendArgs a{K, V, slot_map, K_cache, V_cache, K_scale, V_scale, dev_error, B, n, h,
+               d_h, d_vh, n_blocks, block_tokens};
+  return cache_append(a, dt, static_cast<cudaStream_t>(stream));
+}
+
+size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_kv, int d_h, int d_vh) {
+  if (B <= 0 || n_q <= 0 || h <= 0 || h_kv <= 0 || h % h_kv || d_h <= 0 || d_vh <= 0) return 0;
+  return cache_attention_workspace_bytes(n_q, h, h_kv, d_vh);
+}
+
+mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V_cache,
+                               const float* K_scale, const float* V_scale,
+                               const int32_t* block_table, const int32_t* total_len,
+                               const int32_t* new_len, void* Z, int B, int n_q, int h, int h_kv,
+                               int d_h, int d_vh, int n_blocks, int max_blocks, int block_tokens,
+                               float c, int causal_tail, mha_dtype dt, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (!Q || !K_cache || !V_cache || !K_scale || !V_scale || !block_table || !total_len || !Z)
+    return MHA_ERR_INVALID_ARG;
+  if (B <= 0 || n_q <= 0 || h <= 0 || h_kv <= 0 || d_h <= 0 || d_vh <= 0 || n_blocks <= 0 ||
+      max_blocks <= 0 || block_tokens <= 0 || h % h_kv)
+    return MHA_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || !isfinite(c)) return MHA_ERR_INVALID_ARG;
+  if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > MHA_MAX_PADDED_BATCH)
+    return MHA_ERR_UNSUPPORTED;
+  // keys of a sequence, 16-key groups of a batch, output rows: 32-bit counts
+  if (!fits(max_blocks, block_tokens, 1) || !fits(B, max_blocks, block_tokens / 16) ||
+      !fits((long long)B, n_q, h))
+    return MHA_ERR_UNSUPPORTED;
+  if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(Z))
+    return MHA_ERR_UNSUPPORTED;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < mha_attention_cache_workspace_size(B, n_q, h, h_kv, d_h, d_vh))
+    return MHA_ERR_WORKSPACE;
+  CacheAttnArgs a{Q, K_cache, V_cache, K_scale, V_scale, block_table, total_len, new_len, Z,
+                  workspace, dev_error, B, n_q, h, h_kv, d_h, d_vh, n_blocks, block_tokens,
+                  max_blocks, causal_tail ? 1 : 0, c};
+  return cache_attention(a, dt, static_cast<cudaStream_t>(stream));
+}
+
 mha_status mha_get_device_error(void* error_word, void* stream) {
   if (!error_word) return MHA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -602,6 +753,7 @@ const char* mha_status_string(mha_status s) {
     case MHA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case MHA_ERR_CUDA: return "CUDA runtime or launch error";
     case MHA_ERR_DEVICE_TIMEOUT: return "a kernel gave up waiting on one of its barriers";
+    case MHA_ERR_CACHE_FULL: return "too few free cache blocks for every sequence's new rows";
   }
   return "unknown status";
 }

@@ -23,6 +23,7 @@ STATUS_NAMES = {
     4: "MHA_ERR_WORKSPACE",
     5: "MHA_ERR_CUDA",
     6: "MHA_ERR_DEVICE_TIMEOUT",
+    7: "MHA_ERR_CACHE_FULL",
 }
 MASKS = {"none": 0, "causal": 1, "padding": 2, "causal_padding": 3}
 DTYPES = {"f32": 0, "bf16": 1}
@@ -35,7 +36,9 @@ EXPORTS = (
     "mha_selftest_wait_timeout", "mha_kernel_launch_count", "mha_version",
     "mha_forward_no_alloc", "mha_forward_general", "mha_decode_workspace_size",
     "mha_attention_decode", "mha_attention_plan", "mha_attention_split_workspace_size",
-    "mha_attention_split",
+    "mha_attention_split", "mha_rotary_steps", "mha_rotary", "mha_cache_reserve",
+    "mha_cache_release", "mha_cache_append", "mha_attention_cache_workspace_size",
+    "mha_attention_cache",
 )
 
 _lib = None
@@ -93,6 +96,20 @@ def load(path=LIB_PATH):
     lib.mha_attention_split_workspace_size.argtypes = [I] * 7
     lib.mha_attention_split.restype = I
     lib.mha_attention_split.argtypes = [P] * 4 + [I] * 6 + [F, I, P, I, I, I, P, S, P, P]
+    lib.mha_rotary_steps.restype = I
+    lib.mha_rotary_steps.argtypes = [P, I, ctypes.c_double, I, P]
+    lib.mha_rotary.restype = I
+    lib.mha_rotary.argtypes = [P] * 5 + [I] + [P] * 2 + [I] * 8 + [P]
+    lib.mha_cache_reserve.restype = I
+    lib.mha_cache_reserve.argtypes = [P] * 8 + [I] * 5 + [P] * 2
+    lib.mha_cache_release.restype = I
+    lib.mha_cache_release.argtypes = [P] * 7 + [I] * 4 + [P] * 2
+    lib.mha_cache_append.restype = I
+    lib.mha_cache_append.argtypes = [P] * 7 + [I] * 8 + [P] * 2
+    lib.mha_attention_cache_workspace_size.restype = S
+    lib.mha_attention_cache_workspace_size.argtypes = [I] * 6
+    lib.mha_attention_cache.restype = I
+    lib.mha_attention_cache.argtypes = [P] * 9 + [I] * 9 + [F, I, I, P, S, P, P]
     _lib = lib
     return lib
 
@@ -369,6 +386,216 @@ def attention_decode(Q, K, V, c, cache_len=None, causal_tail=False, out=None, wo
                                   _stream(stream))
     del keep
     _check(st, "mha_attention_decode")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the 8-bit key/value cache
+# ---------------------------------------------------------------------------
+
+# the element types of a cache tensor: bytes of e4m3
+CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _cuda(name, t, dtype, shape, device):
+    """The data pointer of a tensor that must be contiguous, of this type and
+    shape and on this device."""
+    if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError("%s: %s expected, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s: on %s, expected on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s: must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _queue(device, stream):
+    """The stream handle of a call on `device`, which must be the current one:
+    kernels run on the current device."""
+    if device.type != "cuda":
+        raise ValueError("CUDA tensors expected, got a tensor on %s" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is %d"
+                         % (device, torch.cuda.current_device()))
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _scratch(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`: kept by the allocator until that
+    stream has passed the call, even if it is not the current one."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _dtype(t):
+    if t.dtype not in TORCH_DTYPES:
+        raise ValueError("float32 or bfloat16 expected, got %s" % t.dtype)
+    return DTYPES[TORCH_DTYPES[t.dtype]]
+
+
+def _ints(values):
+    return (ctypes.c_int32 * len(values))(*values)
+
+
+def rotary_steps(sections, base=10000.0, per_axis=False, device="cuda"):
+    """The frequency table of rotary(): an int64 tensor with one entry per
+    pair (the bits of the uint64 of mha_rotary_steps). sections: pairs of each
+    axis; per_axis: a ladder of frequencies for each axis instead of one."""
+    out = torch.empty(max(1, sum(max(0, int(m)) for m in sections)), dtype=torch.int64)
+    _check(load().mha_rotary_steps(_ints([int(m) for m in sections]), len(sections), float(base),
+                                   int(bool(per_axis)), out.data_ptr()), "mha_rotary_steps")
+    return out.to(device)
+
+
+def rotary(Q, K, positions, steps, sections, interleaved=False, inverse=False, out=None,
+           stream=None):
+    """mha_rotary: Q (B, h, T, d) and K (B, h_kv, T, d) (or None) turned by
+    their positions (n_axes, B, T), int32; steps from rotary_steps(sections).
+    inverse=True undoes it and is its backward pass. out: (Q_out, K_out), which
+    may be (Q, K). Returns (Q_out, K_out)."""
+    lib = load()
+    B, h, T, d = Q.shape
+    dev, dt = Q.device, _dtype(Q)
+    s = _queue(dev, stream)
+    if out is None:
+        out = (_scratch(Q.shape, Q.dtype, dev, stream),
+               None if K is None else _scratch(K.shape, K.dtype, dev, stream))
+    Qo, Ko = out
+    n_axes, h_kv, kp, kop = len(sections), 0, None, None
+    if K is not None:
+        h_kv = K.shape[1]
+        kp = _cuda("K", K, Q.dtype, (B, h_kv, T, d), dev)
+        kop = _cuda("out[1]", Ko, Q.dtype, (B, h_kv, T, d), dev)
+    st = lib.mha_rotary(_cuda("Q", Q, Q.dtype, Q.shape, dev), kp,
+                        _cuda("positions", positions, torch.int32, (n_axes, B, T), dev),
+                        _cuda("steps", steps, torch.int64, (sum(sections),), dev),
+                        _ints(sections), n_axes, _cuda("out[0]", Qo, Q.dtype, Q.shape, dev), kop,
+                        B, T, h, h_kv, d, 1 if interleaved else 0, 1 if inverse else 0, dt, s)
+    _check(st, "mha_rotary")
+    return Qo, Ko
+
+
+def cache_reserve(cached_len, new_len, free_blocks, n_free, block_table, block_tokens, n,
+                  out=None, dev_error=None, stream=None):
+    """mha_cache_reserve: blocks for the new rows of every sequence, entered in
+    block_table (B, max_blocks) in place, and the rows' slots. free_blocks: the
+    stack of free block numbers, n_free (1,) how many of them are free; all
+    int32. out: (total_len (B,), slot_map (B, n) int64, n_free_out (1,)) to
+    write into. Returns them."""
+    lib = load()
+    B, max_blocks = block_table.shape
+    dev, i32 = block_table.device, torch.int32
+    s = _queue(dev, stream)
+    if out is None:
+        out = (_scratch((B,), i32, dev, stream), _scratch((B, n), torch.int64, dev, stream),
+               _scratch((1,), i32, dev, stream))
+    total_len, slot_map, n_free_out = out
+    n_blocks = free_blocks.numel()
+    st = lib.mha_cache_reserve(_cuda("cached_len", cached_len, i32, (B,), dev),
+                               _cuda("new_len", new_len, i32, (B,), dev),
+                               _cuda("free_blocks", free_blocks, i32, (n_blocks,), dev),
+                               _cuda("n_free", n_free, i32, (1,), dev),
+                               _cuda("block_table", block_table, i32, (B, max_blocks), dev),
+                               _cuda("slot_map", slot_map, torch.int64, (B, n), dev),
+                               _cuda("total_len", total_len, i32, (B,), dev),
+                               _cuda("n_free_out", n_free_out, i32, (1,), dev), B, n, n_blocks,
+                               max_blocks, block_tokens, _word(dev_error, dev), s)
+    _check(st, "mha_cache_reserve")
+    return out
+
+
+def _word(dev_error, device):
+    return None if dev_error is None else _cuda("dev_error", dev_error, torch.int32, (1,), device)
+
+
+def cache_release(cached_len, finished, free_blocks, n_free, block_table, block_tokens, out=None,
+                  dev_error=None, stream=None):
+    """mha_cache_release: the blocks of the sequences with finished[b] != 0 go
+    back on the free stack. out: (total_len (B,), n_free_out (1,)) to write
+    into. Returns them."""
+    lib = load()
+    B, max_blocks = block_table.shape
+    dev, i32 = block_table.device, torch.int32
+    s = _queue(dev, stream)
+    if out is None:
+        out = (_scratch((B,), i32, dev, stream), _scratch((1,), i32, dev, stream))
+    total_len, n_free_out = out
+    n_blocks = free_blocks.numel()
+    st = lib.mha_cache_release(_cuda("cached_len", cached_len, i32, (B,), dev),
+                               _cuda("finished", finished, i32, (B,), dev),
+                               _cuda("free_blocks", free_blocks, i32, (n_blocks,), dev),
+                               _cuda("n_free", n_free, i32, (1,), dev),
+                               _cuda("block_table", block_table, i32, (B, max_blocks), dev),
+                               _cuda("total_len", total_len, i32, (B,), dev),
+                               _cuda("n_free_out", n_free_out, i32, (1,), dev), B, n_blocks,
+                               max_blocks, block_tokens, _word(dev_error, dev), s)
+    _check(st, "mha_cache_release")
+    return out
+
+
+def cache_append(K, V, slot_map, K_cache, V_cache, K_scale, V_scale, dev_error=None, stream=None):
+    """mha_cache_append: rows K (B, h, n, d_h), V (B, h, n, d_vh) into the
+    slots slot_map (B, n), int64, of the cache K_cache (n_blocks, h,
+    block_tokens, d_h), V_cache (n_blocks, h, block_tokens, d_vh) (uint8 or
+    float8_e4m3fn) with its scales (n_blocks, h), all in place."""
+    lib = load()
+    B, h, n, d_h = K.shape
+    d_vh = V.shape[3]
+    n_blocks, bt = K_cache.shape[0], K_cache.shape[2]
+    dev, dt, f32 = K.device, _dtype(K), torch.float32
+    s = _queue(dev, stream)
+    st = lib.mha_cache_append(_cuda("K", K, K.dtype, (B, h, n, d_h), dev),
+                              _cuda("V", V, K.dtype, (B, h, n, d_vh), dev),
+                              _cuda("slot_map", slot_map, torch.int64, (B, n), dev),
+                              _cuda("K_cache", K_cache, CACHE_DTYPES, (n_blocks, h, bt, d_h), dev),
+                              _cuda("V_cache", V_cache, CACHE_DTYPES, (n_blocks, h, bt, d_vh), dev),
+                              _cuda("K_scale", K_scale, f32, (n_blocks, h), dev),
+                              _cuda("V_scale", V_scale, f32, (n_blocks, h), dev), B, n, h, d_h,
+                              d_vh, n_blocks, bt, dt, _word(dev_error, dev), s)
+    _check(st, "mha_cache_append")
+
+
+def attention_cache_workspace_size(B, n_q, h, h_kv, d_h, d_vh):
+    return int(load().mha_attention_cache_workspace_size(B, n_q, h, h_kv, d_h, d_vh))
+
+
+def attention_cache(Q, K_cache, V_cache, K_scale, V_scale, block_table, total_len, c,
+                    new_len=None, causal_tail=False, out=None, workspace=None, dev_error=None,
+                    stream=None):
+    """mha_attention_cache: Z (B, n_q, h*d_vh) for the new query rows Q
+    (B, h, n_q, d_h) over the 8-bit cache (as cache_append fills it) through
+    block_table (B, max_blocks); total_len (B,) rows in the cache, new_len (B,)
+    query rows of each sequence (None: n_q), both int32 on the GPU."""
+    lib = load()
+    B, h, n_q, d_h = Q.shape
+    n_blocks, h_kv, bt, d_vh = V_cache.shape
+    max_blocks = block_table.shape[1]
+    dev, dt, f32, i32 = Q.device, _dtype(Q), torch.float32, torch.int32
+    s = _queue(dev, stream)
+    if out is None:
+        out = _scratch((B, n_q, h * d_vh), Q.dtype, dev, stream)
+    if workspace is None:
+        nbytes = attention_cache_workspace_size(B, n_q, h, h_kv, d_h, d_vh)
+        workspace = _scratch((nbytes,), torch.uint8, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous, on %s" % dev)
+    st = lib.mha_attention_cache(
+        _cuda("Q", Q, Q.dtype, Q.shape, dev),
+        _cuda("K_cache", K_cache, CACHE_DTYPES, (n_blocks, h_kv, bt, d_h), dev),
+        _cuda("V_cache", V_cache, CACHE_DTYPES, (n_blocks, h_kv, bt, d_vh), dev),
+        _cuda("K_scale", K_scale, f32, (n_blocks, h_kv), dev),
+        _cuda("V_scale", V_scale, f32, (n_blocks, h_kv), dev),
+        _cuda("block_table", block_table, i32, (B, max_blocks), dev),
+        _cuda("total_len", total_len, i32, (B,), dev),
+        None if new_len is None else _cuda("new_len", new_len, i32, (B,), dev),
+        _cuda("out", out, Q.dtype, (B, n_q, h * d_vh), dev), B, n_q, h, h_kv, d_h, d_vh,
+        n_blocks, max_blocks, bt, float(c), 1 if causal_tail else 0, dt, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _word(dev_error, dev), s)
+    _check(st, "mha_attention_cache")
     return out
 
 

@@ -80,7 +80,8 @@ typedef enum {
   MHA_ERR_EMPTY_ROW = 3,      /* some query row would have no allowed key */
   MHA_ERR_WORKSPACE = 4,      /* workspace NULL, misaligned or smaller than mha_workspace_size */
   MHA_ERR_CUDA = 5,           /* a CUDA runtime call or a launch failed */
-  MHA_ERR_DEVICE_TIMEOUT = 6  /* a kernel gave up waiting on one of its barriers */
+  MHA_ERR_DEVICE_TIMEOUT = 6, /* a kernel gave up waiting on one of its barriers */
+  MHA_ERR_CACHE_FULL = 7      /* device error word only: mha_cache_reserve had too few free blocks */
 } mha_status;
 
 typedef enum {
@@ -101,6 +102,12 @@ typedef enum { MHA_DTYPE_F32 = 0, MHA_DTYPE_BF16 = 1 } mha_dtype;
 
 /* Largest split over the keys mha_attention_split and mha_attention_plan take. */
 #define MHA_MAX_KEY_SPLITS 256
+
+/* Most position axes of mha_rotary. */
+#define MHA_MAX_ROTARY_AXES 4
+
+/* Most rows per block of the 8-bit key/value cache. */
+#define MHA_MAX_BLOCK_TOKENS 1024
 
 /*
  * Bytes of device workspace mha_forward needs for these sizes: the head-split
@@ -377,6 +384,203 @@ MHA_API mha_status mha_attention_decode(const void* Q, const void* K, const void
                                         float c, const int32_t* cache_len, int causal_tail,
                                         mha_dtype dt, void* workspace, size_t workspace_bytes,
                                         void* stream);
+
+/*
+ * Rotary positions with several axes, and a key/value cache in 8 bits.
+ *
+ * The five operators below stand between mha_qkv_projection (or any source of
+ * head-split Q, K, V) and mha_output_projection: mha_rotary turns Q and K by
+ * their positions, mha_cache_reserve finds blocks and slots for the new rows,
+ * mha_cache_append writes K and V there in 8 bits, mha_attention_cache reads
+ * them, and mha_cache_release gives a finished sequence's blocks back. What
+ * changes from step to step (lengths, block table, slots, free blocks) is on
+ * the device, so a step captured in a CUDA graph is replayed as the sequences
+ * grow. The pages define none of them.
+ *
+ * The cache. Keys K_cache (n_blocks, h_kv, block_tokens, d_h) and values
+ * V_cache (n_blocks, h_kv, block_tokens, d_vh) are bytes of e4m3 (sign, 4
+ * exponent bits of bias 7, 3 mantissa bits; largest 448; 0x7f and 0xff are
+ * NaN), K_scale and V_scale (n_blocks, h_kv) fp32: a value is its e4m3 number
+ * times its block's and head's scale. block_table (B, max_blocks) int32:
+ * position p of sequence b is row p % block_tokens of block
+ * block_table[b][p / block_tokens]. block_tokens is a multiple of 16 up to
+ * MHA_MAX_BLOCK_TOKENS, d_h and d_vh are multiples of 16 up to 256. h_kv may
+ * be any divisor of the query heads h: query head j reads key/value head
+ * j / (h / h_kv).
+ *
+ * What the host cannot check is checked on the device: lengths outside their
+ * range are held to it, and blocks or slots outside the cache are neither read
+ * nor written; either records MHA_ERR_INVALID_ARG in dev_error (a device
+ * int32, or NULL; see mha_get_device_error), which keeps its first entry.
+ */
+
+/*
+ * The frequency table of mha_rotary, computed on the host: `steps` gets one
+ * uint64 per pair, the fraction of a turn that the pair turns per position,
+ * times 2^64. sections: pairs of each axis (n_axes of them, each >= 0).
+ * With P pairs in all, pair i turns by base^(-i/P) radians per position
+ * (per_axis = 0: one ladder over all pairs, whichever axis a pair belongs to)
+ * or pair j of an axis of m pairs by base^(-j/m) (per_axis = 1: a ladder per
+ * axis). A caller may fill the table with frequencies of its own instead:
+ * steps[i] = w_i / (2 pi) * 2^64, modulo 2^64.
+ * MHA_ERR_INVALID_ARG for NULL, a negative section, no pair, base <= 0 or not
+ * finite; MHA_ERR_UNSUPPORTED for more than MHA_MAX_ROTARY_AXES axes or 128
+ * pairs.
+ */
+MHA_API mha_status mha_rotary_steps(const int32_t* sections, int n_axes, double base,
+                                    int per_axis, uint64_t* steps);
+
+/*
+ * Rotary positions: pair i of every row of Q and K turns by the angle
+ * positions[axis(i)][b][t] * w_i, (x, y) -> (x cos - y sin, x sin + y cos).
+ *
+ *   Q (B, h, T, d), K (B, h_kv, T, d) or NULL; Q_out, K_out of the same shapes
+ *                 (K_out NULL with K); an output may be its own input (in
+ *                 place) and must not overlap anything else
+ *   positions     device int32 (n_axes, B, T): time, height, width, ...; any
+ *                 values, negative ones too
+ *   steps         DEVICE copy of the table of mha_rotary_steps
+ *   sections      HOST int32[n_axes]: the first sections[0] pairs turn with
+ *                 axis 0, the next sections[1] with axis 1, ...; their sum P
+ *                 is at most d / 2
+ *   interleaved   0: pair i is columns (i, i + P); 1: columns (2i, 2i + 1).
+ *                 Columns 2P and up are left as they are (copied)
+ *   inverse       1: turns by the opposite angles, which undoes the call and is
+ *                 its backward pass: the gradient with respect to the inputs
+ *                 is the inverse applied to that of the outputs
+ *
+ * The angle is reduced exactly (an integer product modulo one turn), so far
+ * positions are as exact as near ones; sines and cosines in fp32, one
+ * rounding to the element type. d even, at most 256; pointers 16-byte aligned;
+ * h + h_kv at most 65535 (MHA_ERR_UNSUPPORTED otherwise). One kernel.
+ */
+MHA_API mha_status mha_rotary(const void* Q, const void* K, const int32_t* positions,
+                              const uint64_t* steps, const int32_t* sections, int n_axes,
+                              void* Q_out, void* K_out, int B, int T, int h, int h_kv, int d,
+                              int interleaved, int inverse, mha_dtype dt, void* stream);
+
+/*
+ * Blocks and slots for new rows, from the sequences' lengths, on the GPU.
+ *
+ *   cached_len (B)   rows that each sequence has in the cache
+ *   new_len (B)      rows to add, each in [0, n]
+ *   free_blocks      (n_blocks) a stack of free block numbers, of which the
+ *                    first *n_free are free; taken from the top (the end)
+ *   block_table      (B, max_blocks): the entries of the new blocks are
+ *                    written, the others left as they are
+ *   slot_map         out (B, n) int64: new row i of sequence b is row
+ *                    slot_map[b][i] % block_tokens of block
+ *                    slot_map[b][i] / block_tokens; -1 for i >= new_len[b]
+ *   total_len (B)    out: cached_len + new_len, the next call's cached_len
+ *   n_free_out       out: free blocks left, the next call's n_free
+ *
+ * All device int32 but slot_map. Sequences are served in order, always with
+ * the same result: one whose new blocks no longer fit beside those of all
+ * sequences before it gets none of its rows (slots -1, total_len =
+ * cached_len) and MHA_ERR_CACHE_FULL is recorded in dev_error; one that needs
+ * no new block is always served. A sequence with a negative length, more than
+ * n new rows or more than max_blocks blocks gets none of its rows either, and
+ * MHA_ERR_INVALID_ARG is recorded. total_len and n_free_out must not be the
+ * inputs themselves (MHA_ERR_INVALID_ARG). B at most MHA_MAX_PADDED_BATCH.
+ * One kernel.
+ */
+MHA_API mha_status mha_cache_reserve(const int32_t* cached_len, const int32_t* new_len,
+                                     const int32_t* free_blocks, const int32_t* n_free,
+                                     int32_t* block_table, int64_t* slot_map,
+                                     int32_t* total_len, int32_t* n_free_out, int B, int n,
+                                     int n_blocks, int max_blocks, int block_tokens,
+                                     int32_t* dev_error, void* stream);
+
+/*
+ * Gives back the blocks of the sequences b with finished[b] != 0: their
+ * block_table entries go on top of the free stack, in order of the sequences,
+ * and total_len[b] is 0 (cached_len[b] for the others). The table is left as
+ * it is. Blocks must not be given back twice: a call that would make more
+ * than n_blocks free records MHA_ERR_INVALID_ARG and gives back only the
+ * sequences that fit. Other arguments as for mha_cache_reserve. One kernel.
+ */
+MHA_API mha_status mha_cache_release(const int32_t* cached_len, const int32_t* finished,
+                                     int32_t* free_blocks, const int32_t* n_free,
+                                     const int32_t* block_table, int32_t* total_len,
+                                     int32_t* n_free_out, int B, int n_blocks, int max_blocks,
+                                     int block_tokens, int32_t* dev_error, void* stream);
+
+/*
+ * Writes new rows to the cache in 8 bits.
+ *
+ *   K (B, h, n, d_h), V (B, h, n, d_vh)   new rows (h: key/value heads)
+ *   slot_map (B, n)   as mha_cache_reserve writes it: the rows of a batch item
+ *                     that are written come first, in consecutive positions;
+ *                     rows with slot -1 are not written. No two batch items
+ *                     share a block. A row whose slot does not follow the row
+ *                     before it is not written (MHA_ERR_INVALID_ARG in
+ *                     dev_error)
+ *
+ * A block's scale is the smallest power of two s (at least 2^-126) with
+ * |x| / s <= 448 for all its rows, and every value is rounded once, to the
+ * nearest e4m3, ties to even. The rows of a block before the first new one are
+ * kept: the scale is then at least what it was, and where it grows these rows
+ * are rounded again to the new scale. Infinities become +-448 s and do not
+ * count for s; NaN stays NaN. d_h and d_vh multiples of 16 up to 256,
+ * block_tokens a multiple of 16, B at most 32767, h at most 65535, pointers
+ * 16-byte aligned (MHA_ERR_UNSUPPORTED otherwise). One kernel.
+ */
+MHA_API mha_status mha_cache_append(const void* K, const void* V, const int64_t* slot_map,
+                                    void* K_cache, void* V_cache, float* K_scale,
+                                    float* V_scale, int B, int n, int h, int d_h, int d_vh,
+                                    int n_blocks, int block_tokens, mha_dtype dt,
+                                    int32_t* dev_error, void* stream);
+
+/*
+ * Device scratch of mha_attention_cache, in bytes: the summaries of the pieces
+ * that tiles of up to 16 query rows are cut into, at most two per warp of the
+ * grid. It does not depend on B or on any length. 0 when an argument is
+ * non-positive or h_kv does not divide h.
+ */
+MHA_API size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_kv, int d_h,
+                                                  int d_vh);
+
+/*
+ * Attention of new query rows over the 8-bit cache.
+ *
+ *   Q (B, h, n_q, d_h)   the new rows, head-split
+ *   total_len (B)        device int32: rows that each sequence has in the cache,
+ *                        its new ones included; 0 and up
+ *   new_len (B)          device int32 or NULL (n_q everywhere): query rows of
+ *                        each sequence; rows i >= new_len[b] are padding, their
+ *                        rows of Z are zeros
+ *   Z (B, n_q, h*d_vh)   output, concatenated layout (as mha_attention)
+ *   causal_tail          0: every row sees all total_len[b] keys. 1: the rows
+ *                        are the last new_len[b] positions of the sequence, and
+ *                        row i sees keys j <= total_len[b] - new_len[b] + i.
+ *                        A row that sees no key is zeros
+ *   workspace            device scratch of mha_attention_cache_workspace_size
+ *                        bytes, 256-byte aligned, contents on entry irrelevant;
+ *                        calls that share it must not overlap on the GPU
+ *
+ * Scores, weights and sums in fp32; in the products the cache's numbers are
+ * exact, bf16 queries too, and weights have 11 bits (22 with MHA_DTYPE_F32,
+ * queries as well). Cache rows at positions >= total_len[b] are never read,
+ * and a NaN in a row does not reach the query rows that do not see it.
+ * Built for few query rows per key/value head (generated or drafted tokens):
+ * 16 rows, n_q * h / h_kv, share one pass over the cache.
+ *
+ * MHA_ERR_INVALID_ARG for NULL pointers, non-positive sizes, h not a multiple
+ * of h_kv, non-finite c; MHA_ERR_UNSUPPORTED for other head or block sizes
+ * than above, B above MHA_MAX_PADDED_BATCH, more than 2^31 - 1 keys per
+ * sequence, 16-key groups per batch or rows of Z, misaligned pointers;
+ * MHA_ERR_WORKSPACE for a missing, misaligned or small workspace. Enqueues two
+ * kernels.
+ */
+MHA_API mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V_cache,
+                                       const float* K_scale, const float* V_scale,
+                                       const int32_t* block_table, const int32_t* total_len,
+                                       const int32_t* new_len, void* Z, int B, int n_q, int h,
+                                       int h_kv, int d_h, int d_vh, int n_blocks,
+                                       int max_blocks, int block_tokens, float c,
+                                       int causal_tail, mha_dtype dt, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_error,
+                                       void* stream);
 
 /* Size of the device scratch built into the library for mha_forward_no_alloc. */
 #define MHA_NO_ALLOC_SCRATCH_BYTES (32u << 20)
