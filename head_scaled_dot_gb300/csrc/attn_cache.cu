@@ -59,6 +59,8 @@ constexpr int CA_HEADER = 8192;    // workspace: first group of every batch item
 constexpr int CM_THREADS = 128;    // merge kernel
 
 struct CacheAttnParams {
+  CUtensorMap map_k;    // K as (d_h, bt, n_blocks h_kv) bytes
+  CUtensorMap map_v;
   const void* Q;        // (B, h, n_q, d_h)
   const uint8_t* K;     // (n_blocks, h_kv, bt, d_h)
   const uint8_t* V;     // (n_blocks, h_kv, bt, d_vh)
@@ -77,20 +79,16 @@ struct CacheAttnParams {
   int causal_tail;
   int warps;            // W
   float cl2;            // c log2(e)
+  uint64_t limit_ns;    // bounded waits give up after this long
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(full ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* m, uint64_t* bar,
+                                               int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -136,6 +134,21 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// z tile n += P v for the rows that are kept (rows g + 8 only with RH = 2).
+template <int RH, int NT>
+__device__ __forceinline__ void mma_rows(float (&z)[RH][NT][2], int n, const uint32_t (&p)[2][2],
+                                         uint32_t b0, uint32_t b1) {
+  float c[4] = {z[0][n][0], z[0][n][1], RH == 2 ? z[RH - 1][n][0] : 0.f,
+                RH == 2 ? z[RH - 1][n][1] : 0.f};
+  mma_f16(c, p[0][0], p[1][0], p[0][1], p[1][1], b0, b1);
+  z[0][n][0] = c[0];
+  z[0][n][1] = c[1];
+  if constexpr (RH == 2) {
+    z[RH - 1][n][0] = c[2];
+    z[RH - 1][n][1] = c[3];
+  }
+}
+
 // Two floats as fp16 (hi), and what that rounding left out as fp16 (lo).
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -158,30 +171,47 @@ __device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& b
   return Item{min(max(t, 0), most), min(max(f, 0), P.n_q)};
 }
 
-// Stage layout for rows of D bytes: SK key rows, SK value rows, then per
-// 16-key group {ks, vs, valid, 0}.
+// A warp's stage: SK key rows and SK value rows of D bytes, each side as
+// D / 128 planes (one of 64 bytes for D = 64) of SK rows, written by TMA with
+// the swizzle of that width. Beside it per 16 keys {ks, vs, block found}.
 template <int D>
 struct Stage {
-  static constexpr int SK = D == 256 ? 16 : 32;  // keys
+  static constexpr int SK = D == 256 ? 16 : 32;    // keys
   static constexpr int SUBS = SK / 16;
-  static constexpr int ROWS = SK * D;            // bytes of one side
-  static constexpr int BYTES = 2 * ROWS + 16 * SUBS;
-  static constexpr int N = D == 64 ? 6 : 3;      // stages per warp
-  static constexpr int SMEM = CA_WARPS * N * BYTES + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int WIDTH = D == 64 ? 64 : 128; // bytes of a plane's row
+  static constexpr int PLANE = SK * WIDTH;
+  static constexpr int ROWS = SK * D;              // bytes of one side
+  static constexpr int BYTES = 2 * ROWS;
+  static constexpr int N = D == 64 ? 6 : 3;        // stages per warp
+  static constexpr int RING = CA_WARPS * N * BYTES;
+  static constexpr int META = CA_WARPS * N * SUBS * 16;
+  static constexpr int BARS = CA_WARPS * N * 8;
+  static constexpr int SMEM = 1024 + RING + META + BARS + (MHA_MAX_PADDED_BATCH + 8) * 4;
 };
 
-// Byte offset of 16-byte piece c of row k, swizzled: the reads of eight lanes
-// at a time (key rows 2p, 2p + 1 and four neighbouring pieces; or value rows
-// 0, 2, 4, 6 or 1, 3, 5, 7 and two neighbouring pieces) touch each bank once.
+// Which key of a tile of 8 is column n of the score tile (and so which rows
+// the value operand takes): the order in which the swizzled rows are read
+// without bank conflicts. Eight lanes read at a time: key rows key_of(2p),
+// key_of(2p + 1) and four neighbouring 16-byte pieces, or value rows
+// key_of(2t + e), t = 0 .. 3, and two neighbouring pieces.
+template <int D>
+__device__ __forceinline__ int key_of(int n) {
+  const int e = n & 1, t = n >> 1;
+  if constexpr (D == 64) {
+    const int k = (t & 1) | (t >> 1) << 2;  // 0, 1, 4, 5
+    return e ? k ^ 3 : k;
+  } else {
+    return e ? ((2 * t) ^ 4) | 1 : 2 * t;
+  }
+}
+
+// Byte offset of 16-byte piece c of row k of one side.
 template <int D>
 __device__ __forceinline__ uint32_t piece_at(int k, int c) {
-  if constexpr (D == 64) {
-    const int line = k >> 1;
-    return (uint32_t)(line * 128 + (((((k & 1) << 2) | c) ^ ((line & 3) << 1)) << 4));
-  } else {
-    const int f = (k & 2) | (((k ^ (k >> 2)) & 1) << 2);
-    return (uint32_t)(k * D + ((c & 8) << 4) + (((c & 7) ^ f) << 4));
-  }
+  if constexpr (D == 64)
+    return (uint32_t)(k * 64 + ((c ^ ((k >> 1) & 3)) << 4));
+  else
+    return (uint32_t)((c >> 3) * Stage<D>::PLANE + k * 128 + (((c & 7) ^ (k & 7)) << 4));
 }
 
 // Where a warp is in the list of groups.
@@ -193,13 +223,26 @@ template <int D, int RH, bool F32>
 __global__ void __launch_bounds__(CA_THREADS, 1)
     cache_attention_kernel(const __grid_constant__ CacheAttnParams P) {
   using S = Stage<D>;
-  constexpr int NT = D / 8;   // output tiles of 8 columns
-  constexpr int KC = D / 64;  // 16-byte pieces of a key row per lane
-  extern __shared__ __align__(128) unsigned char smem[];
-  int* first = reinterpret_cast<int*>(smem + CA_WARPS * S::N * S::BYTES);  // (B + 1)
+  constexpr int NT = D / 8;        // output tiles of 8 columns
+  constexpr int KC = D / 64;       // 16-byte pieces of a key row per lane
+  constexpr int SN = S::SK / 8;    // score tiles of 8 keys per group
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::RING + S::META);
+  int* first = reinterpret_cast<int*>(smem + S::RING + S::META + S::BARS);  // (B + 1)
   __shared__ int warp_sums[CA_WARPS];
+  __shared__ int abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
+  uint64_t* full = bars + warp * S::N;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    tma_prefetch_desc(&P.map_k);
+    tma_prefetch_desc(&P.map_v);
+  }
+  if (lane < S::N) mbar_init(full + lane, 1);
+  fence_mbar_init();
 
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -248,9 +291,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   const int unit = P.h_kv * P.tiles;
   const long long G = (long long)first[P.B] * unit;
   const int w = blockIdx.x * CA_WARPS + warp;
-  long long g0 = w * G / P.warps;
+  const long long g0 = w * G / P.warps;
   const long long g1 = (w + 1) * G / P.warps;
   if (g0 >= g1) return;
+  const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   Cursor cc;  // what is computed
   {
@@ -265,67 +309,109 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     cc.pr = (int)(in / cc.ng);
     cc.gi = (int)(in - (long long)cc.pr * cc.ng);
   }
-  Cursor lc = cc;  // what is loaded
-  long long left = g1 - g0, load_left = left;
+  int left = (int)(g1 - g0), load_left = left;
+  // true when the cursor has moved to another tile of rows
   auto advance = [&](Cursor& c) {
-    if (++c.gi < c.ng) return;
+    if (++c.gi < c.ng) return false;
     c.gi = 0;
-    if (++c.pr < unit) return;
+    if (++c.pr < unit) return true;
     c.pr = 0;
     do {
       ++c.b;
     } while (c.b < P.B && first[c.b + 1] == first[c.b]);
     c.ng = c.b < P.B ? first[c.b + 1] - first[c.b] : 1;
+    return true;
   };
 
   const uint32_t ring = smem_u32(smem) + warp * S::N * S::BYTES;
-  // table entries [win, win + 32) of item win_b, one per lane
-  int win = 0, win_b = -1, win_id = 0, load_total = 0;
+  const uint32_t metas = smem_u32(smem) + S::RING + warp * S::N * S::SUBS * 16;
+
+  // What is loaded: the cursor, its place in the block table and two windows
+  // of 32 table entries, one per lane, the second asked for ahead of its use.
+  Cursor lc = cc;
+  int lj, lrow, lkv, ltotal, win, win_id, next_id;
+  auto table_entry = [&](int j) {
+    return j < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + j) : -1;
+  };
+  auto place = [&]() {  // at a tile's beginning, or this warp's
+    bool bad;
+    const int k0 = lc.gi * S::SK;
+    ltotal = item_of(P, lc.b, bad).total;
+    lkv = lc.pr / P.tiles;
+    lj = k0 / P.bt;
+    lrow = k0 - lj * P.bt;
+    win = lj;
+    win_id = table_entry(win + lane);
+    next_id = table_entry(win + 32 + lane);
+  };
+  place();
+  // the scales asked for with a group's rows: {ks, vs} of each 16 keys, one
+  // per lane, put beside the stage one step later
+  float held = 0.f;
+  int held_meta = -1;
+  auto put_scales = [&]() {
+    if (held_meta >= 0 && lane < 2 * S::SUBS)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(metas + held_meta * S::SUBS * 16 + (lane >> 1) * 16 +
+                                                   (lane & 1) * 4),
+                   "f"(held)
+                   : "memory");
+    held_meta = -1;
+  };
   auto issue = [&](int stage) {
-    const uint32_t dst = ring + stage * S::BYTES;
-    const int k0 = lc.gi * S::SK, kv = lc.pr / P.tiles;
-    const int j0 = k0 / P.bt, j1 = (k0 + S::SK - 1) / P.bt;
-    if (lc.b != win_b || j0 < win || j1 >= win + 32) {
-      if (lc.b != win_b) {
-        bool bad;
-        load_total = item_of(P, lc.b, bad).total;
-      }
-      win_b = lc.b;
-      win = j0;
-      const int j = win + lane;
-      win_id = j < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + j) : -1;
+    if (lj + 1 >= win + 32) {
+      // lane i takes entry lj + i of the two windows (lj - win is 31 or 32)
+      const int at = lane + lj - win;
+      const int x = __shfl_sync(0xffffffffu, win_id, at & 31);
+      const int y = __shfl_sync(0xffffffffu, next_id, at & 31);
+      win_id = at < 32 ? x : y;
+      win = lj;
+      next_id = table_entry(win + 32 + lane);
     }
+    const uint32_t dst = ring + stage * S::BYTES;
+    const int k0 = lc.gi * S::SK;
+    int blk[S::SUBS], row[S::SUBS];
+    bool ok[S::SUBS];
+    uint32_t bytes = 0;
 #pragma unroll
     for (int sub = 0; sub < S::SUBS; ++sub) {
-      const int k = k0 + 16 * sub, j = k / P.bt;
-      int id = __shfl_sync(0xffffffffu, win_id, j - win);
-      const bool used = k < load_total;
-      const bool ok = used && id >= 0 && id < P.n_blocks;
-      if (used && !ok && P.err && lane == 0) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
-      if (!ok) id = 0;
-      const long long blk = (long long)id * P.h_kv + kv;
-      const int row = k - j * P.bt;
-      const uint8_t* ks = P.K + (blk * P.bt + row) * P.d_h;
-      const uint8_t* vs = P.V + (blk * P.bt + row) * P.d_vh;
-      constexpr int C = D / 16;        // pieces per row
-      constexpr int RPI = 32 / C;      // rows per instruction
-      const int c = lane % C, r0 = lane / C;
-      const int rows = ok ? min(16, load_total - k) : 0;
-#pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = r0 + i * RPI;
-        const bool in = r < rows;
-        const bool kin = in && c * 16 < P.d_h, vin = in && c * 16 < P.d_vh;
-        const uint32_t at = piece_at<D>(16 * sub + r, c);
-        cp_async16(dst + at, kin ? ks + (long long)r * P.d_h + c * 16 : P.K, kin);
-        cp_async16(dst + S::ROWS + at, vin ? vs + (long long)r * P.d_vh + c * 16 : P.V, vin);
+      int id = __shfl_sync(0xffffffffu, win_id, lj - win);
+      const bool used = k0 + 16 * sub < ltotal;
+      ok[sub] = used && id >= 0 && id < P.n_blocks;
+      if (used && !ok[sub] && P.err && lane == 0) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+      blk[sub] = (ok[sub] ? id : 0) * P.h_kv + lkv;
+      row[sub] = lrow;
+      if (ok[sub]) bytes += 2 * 16 * D;
+      lrow += 16;
+      if (lrow >= P.bt) {
+        lrow = 0;
+        ++lj;
       }
-      const uint32_t meta = dst + 2 * S::ROWS + 16 * sub;
-      if (lane == 0) cp_async4(meta, P.Ks + blk);
-      if (lane == 1) cp_async4(meta + 4, P.Vs + blk);
-      if (lane == 2)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + 8), "r"(ok ? 1u : 0u) : "memory");
     }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full + stage, bytes);
+#pragma unroll
+      for (int sub = 0; sub < S::SUBS; ++sub) {
+        if (!ok[sub]) continue;
+#pragma unroll
+        for (int p = 0; p < D / S::WIDTH; ++p) {
+          const uint32_t at = dst + p * S::PLANE + sub * 16 * S::WIDTH;
+          tma_load_3d_at(at, &P.map_k, full + stage, p * 128, row[sub], blk[sub]);
+          tma_load_3d_at(at + S::ROWS, &P.map_v, full + stage, p * 128, row[sub], blk[sub]);
+        }
+      }
+    }
+    // scales and whether the block was found
+    const int sub = lane >> 1;
+#pragma unroll
+    for (int i = 0; i < S::SUBS; ++i) {
+      if (sub != i) continue;
+      held = __ldg((lane & 1 ? P.Vs : P.Ks) + blk[i]);
+      if (!(lane & 1))
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(metas + (stage * S::SUBS + i) * 16 + 8),
+                     "r"(ok[i] ? 1u : 0u)
+                     : "memory");
+    }
+    held_meta = stage;
   };
 
   // the tile's rows: this thread holds rows g and (RH = 2) g + 8
@@ -335,7 +421,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   int lim_all = 0;  // every row that sees keys sees the keys up to here
   int lim_any = -1; // no row sees keys past this
   float m[RH], l[RH], z[RH][NT][2];
-  bool piece_starts = true;
+  float vref = 1.f, vtop = 0.f;  // z is in units of vref 2^-13; largest vs so far
   int start_gi = 0;
 
   auto begin_tile = [&]() {
@@ -396,7 +482,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       int E = (int)(__float_as_uint(top) >> 23) - 127;
       E = E > 127 || top == 0.f ? 14 : max(E, -100);
       const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-      qf[rh] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+      qf[rh] = P.cl2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
 #pragma unroll
@@ -420,162 +506,210 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
     lim_all = lo;
     lim_any = hi;
-    piece_starts = false;
+    vref = 1.f;
+    vtop = 0.f;
     start_gi = cc.gi;
   };
 
   auto fold = [&](int stage) {
     const uint32_t src = ring + stage * S::BYTES;
-#pragma unroll 1
-    for (int sub = 0; sub < S::SUBS; ++sub) {
-      const int kb = cc.gi * S::SK + 16 * sub;
-      if (kb > lim_any) break;
-      const uint4 meta = lds128(src + 2 * S::ROWS + 16 * sub);
-      if (!meta.z) continue;  // no such block
-      // scores
-      float s[2][4];
+    const int kb = cc.gi * S::SK;
+    if (kb > lim_any) return;
+    float ks[S::SUBS], vs[S::SUBS];
+    bool dead[S::SUBS];
+    bool masked = kb + S::SK - 1 > lim_all;
+    float vmost = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        float s2[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < S::SUBS; ++i) {
+      const uint4 meta = lds128(metas + (stage * S::SUBS + i) * 16);
+      ks[i] = __uint_as_float(meta.x);
+      vs[i] = __uint_as_float(meta.y);
+      dead[i] = !meta.z;  // past the end, or no such block
+      if (dead[i]) {
+        masked = true;
+        ks[i] = vs[i] = 0.f;
+      }
+      vmost = fmaxf(vmost, vs[i]);
+    }
+    // scores
+    float s[SN][4];
 #pragma unroll
-        for (int k = 0; k < KC; ++k) {
-          const uint4 u = lds128(src + piece_at<D>(16 * sub + 8 * nt + g, t + 4 * k));
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    for (int nt = 0; nt < SN; ++nt) {
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const uint32_t b0 = e4m3_lo(x[f]), b1 = e4m3_hi(x[f]);
-            const uint32_t(&a)[RH * 2] = qa[4 * k + f];
-            mma_f16(s[nt], a[0], RH == 2 ? a[RH * 2 - 2] : 0u, a[1], RH == 2 ? a[RH * 2 - 1] : 0u, b0, b1);
-            if constexpr (F32) {
-              const uint32_t(&c)[RH * 2] = ql[4 * k + f];
-              mma_f16(s2, c[0], RH == 2 ? c[RH * 2 - 2] : 0u, c[1], RH == 2 ? c[RH * 2 - 1] : 0u, b0, b1);
-            }
+      for (int k = 0; k < KC; ++k) {
+        const uint4 u = lds128(src + piece_at<D>(8 * nt + key_of<D>(g), t + 4 * k));
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const uint32_t b0 = e4m3_lo(x[f]), b1 = e4m3_hi(x[f]);
+          const uint32_t(&a)[RH * 2] = qa[4 * k + f];
+          mma_f16(s[nt], a[0], RH == 2 ? a[RH * 2 - 2] : 0u, a[1], RH == 2 ? a[RH * 2 - 1] : 0u, b0, b1);
+          if constexpr (F32) {
+            const uint32_t(&c)[RH * 2] = ql[4 * k + f];
+            mma_f16(s2, c[0], RH == 2 ? c[RH * 2 - 2] : 0u, c[1], RH == 2 ? c[RH * 2 - 1] : 0u, b0, b1);
           }
         }
-        if constexpr (F32) {
+      }
+      if constexpr (F32) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] += s2[e];
+        for (int e = 0; e < 4; ++e) s[nt][e] += s2[e];
+      }
+    }
+    float mx[RH];
+#pragma unroll
+    for (int rh = 0; rh < RH; ++rh) {
+      mx[rh] = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < SN; ++nt) {
+        const float f = ks[nt / 2] * qf[rh];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& v = s[nt][2 * rh + e];
+          v *= f;
+          if (masked && (kb + 8 * nt + key_of<D>(2 * t + e) > limit[rh] || dead[nt / 2])) v = -INFINITY;
+          mx[rh] = fmaxf(mx[rh], v);
         }
       }
-      // the group's own summary: weights against its maximum
-      const bool masked = kb + 15 > lim_all;
-      const float scale = __uint_as_float(meta.x) * P.cl2;
-      const float vscale = __uint_as_float(meta.y) * 6.103515625e-05f;  // 2^-14
-      uint32_t pa[2][2], pl[2][2];  // [row half][k half]
-      float alpha[RH], beta[RH];
-      bool raised = false;
-      pa[1][0] = pa[1][1] = pl[1][0] = pl[1][1] = 0u;
+    }
+    // The reference m of a row is raised only where a score passes it by more
+    // than 2^2: weights are then at most 2^2.
+    bool raise = mx[0] > m[0] + 2.f;
+    if constexpr (RH == 2) raise |= mx[1] > m[1] + 2.f;
+    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int rh = 0; rh < RH; ++rh) {
-        const float f = scale * qf[rh];
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = s[e >> 1][2 * rh + (e & 1)] * f;
-          if (masked && kb + 8 * (e >> 1) + 2 * t + (e & 1) > limit[rh]) v[e] = -INFINITY;
-        }
-        float mg = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 1));
-        mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, 2));
-        const float mn = fmaxf(m[rh], mg);
-        const float base = mg == -INFINITY ? 0.f : mg;  // an empty group: every weight 0
-        alpha[rh] = mn == m[rh] ? 1.f : ex2_approx(m[rh] - mn);
-        beta[rh] = mg == mn ? 1.f : ex2_approx(mg - mn);
-        if (mg == -INFINITY) beta[rh] = 0.f;
-        raised |= alpha[rh] != 1.f;
+        float top = fmaxf(mx[rh], __shfl_xor_sync(0xffffffffu, mx[rh], 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = top > m[rh] + 2.f ? top : m[rh];
+        const float alpha = mn == m[rh] ? 1.f : ex2_approx(m[rh] - mn);
         m[rh] = mn;
-        float sum = 0.f;
+        l[rh] *= alpha;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = ex2_approx(v[e] - base);
-          sum += v[e];
-          v[e] *= 16384.f;
-        }
-        l[rh] = l[rh] * alpha[rh] + sum * beta[rh];
-        beta[rh] *= vscale;
-        pa[rh][0] = pack_half(v[0], v[1]);
-        pa[rh][1] = pack_half(v[2], v[3]);
-        if constexpr (F32) {
-          pl[rh][0] = rest_half(v[0], v[1], pa[rh][0]);
-          pl[rh][1] = rest_half(v[2], v[3], pa[rh][1]);
+        for (int n = 0; n < NT; ++n) {
+          z[rh][n][0] *= alpha;
+          z[rh][n][1] *= alpha;
         }
       }
-      if (__any_sync(0xffffffffu, raised)) {
+    }
+#pragma unroll
+    for (int rh = 0; rh < RH; ++rh) {
+      const float base = m[rh] == -INFINITY ? 0.f : m[rh];  // nothing seen yet: every weight 0
+#pragma unroll
+      for (int nt = 0; nt < SN; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[nt][2 * rh + e] = ex2_approx(s[nt][2 * rh + e] - base);
+          l[rh] += s[nt][2 * rh + e];
+        }
+      }
+    }
+    // z is kept in units of vref 2^-13 and the weights carry 2^13 vs / vref,
+    // with vs / vref in [2^-4, 1]: at most fp16's 2^15. vref follows vs, a
+    // smaller one down to 2^-60 of the largest only, so that z (at most
+    // 2^13 448 2^2 times the keys) cannot overflow. Two blocks in one group
+    // that are further apart than 2^2 go one after the other.
+    bool split = false;
+    if constexpr (S::SUBS == 2) {
+      const float least = fminf(vs[0], vs[S::SUBS - 1]);
+      split = least > 0.f && least < 0.25f * vmost;
+    }
+    bool nan = false;
+#pragma unroll 1
+    for (int pass = 0; pass < (split ? 2 : 1); ++pass) {
+      const float most = !split ? vmost : pass == 0 ? vs[0] : vs[S::SUBS - 1];
+      const float before = vtop;  // 0: z holds nothing yet
+      vtop = fmaxf(vtop, most);
+      if (most > 0.f && (most > vref || most < 0.25f * vref)) {
+        const float to = fmaxf(most, vtop * 8.6736173798840355e-19f);  // 2^-60
+        if (to != vref) {
+          const float by = before > 0.f ? vref / to : 1.f;
+#pragma unroll
+          for (int rh = 0; rh < RH; ++rh) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              z[rh][n][0] *= by;
+              z[rh][n][1] *= by;
+            }
+          }
+          vref = to;
+        }
+      }
+      // values: rows key_of(2t), key_of(2t + 1), and those + 8, of each 16 keys
+#pragma unroll
+      for (int i = 0; i < S::SUBS; ++i) {
+        const float r = split && i != pass ? 0.f : 8192.f * (vs[i] / vref);
+        uint32_t pa[2][2], pl[2][2];  // [row half][k half]
+        pa[1][0] = pa[1][1] = pl[1][0] = pl[1][1] = 0u;
 #pragma unroll
         for (int rh = 0; rh < RH; ++rh) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            z[rh][n][0] *= alpha[rh];
-            z[rh][n][1] *= alpha[rh];
+          for (int hk = 0; hk < 2; ++hk) {
+            const float p0 = s[2 * i + hk][2 * rh] * r, p1 = s[2 * i + hk][2 * rh + 1] * r;
+            pa[rh][hk] = pack_half(p0, p1);
+            if constexpr (F32) pl[rh][hk] = rest_half(p0, p1, pa[rh][hk]);
           }
         }
-      }
-      // values: rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group
-      bool nan = false;
-      const int vr = 16 * sub + 2 * t;
 #pragma unroll
-      for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-        constexpr int WORDS = D == 64 ? 2 : 4;
-        uint32_t x[4][WORDS];
+        for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
+          constexpr int WORDS = D == 64 ? 2 : 4;
+          uint32_t x[4][WORDS];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = vr + (r & 1) + 8 * (r >> 1);
-          if constexpr (D == 64) {
-            const uint2 u = lds64(src + S::ROWS + piece_at<D>(row, g >> 1) + 8 * (g & 1));
-            x[r][0] = u.x; x[r][1] = u.y;
-          } else {
-            const uint4 u = lds128(src + S::ROWS + piece_at<D>(row, g + 8 * half));
-            x[r][0] = u.x; x[r][1] = u.y; x[r][2] = u.z; x[r][3] = u.w;
-          }
-          if (masked) {
-            // a NaN value must not reach the rows that do not see its key:
-            // it is taken out here and put back below
+          for (int j = 0; j < 4; ++j) {
+            const int row = 16 * i + key_of<D>(2 * t + (j & 1)) + 8 * (j >> 1);
+            if constexpr (D == 64) {
+              const uint2 u = lds64(src + S::ROWS + piece_at<D>(row, g >> 1) + 8 * (g & 1));
+              x[j][0] = u.x; x[j][1] = u.y;
+            } else {
+              const uint4 u = lds128(src + S::ROWS + piece_at<D>(row, g + 8 * half));
+              x[j][0] = u.x; x[j][1] = u.y; x[j][2] = u.z; x[j][3] = u.w;
+            }
+            if (masked) {
+              // a NaN value must not reach the rows that do not see its key:
+              // it is taken out here and put back below
 #pragma unroll
-            for (int q = 0; q < WORDS; ++q) {
-              const uint32_t hit = ((x[r][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              nan |= hit != 0;
-              x[r][q] &= ~((hit >> 7) * 0xffu);
+              for (int q = 0; q < WORDS; ++q) {
+                const uint32_t hit = ((x[j][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                nan |= hit != 0;
+                x[j][q] &= ~((hit >> 7) * 0xffu);
+              }
             }
           }
-        }
 #pragma unroll
-        for (int q = 0; q < WORDS; ++q) {
+          for (int q = 0; q < WORDS; ++q) {
 #pragma unroll
-          for (int hq = 0; hq < 2; ++hq) {
-            const uint32_t sel = hq ? 0x7362u : 0x5140u;
-            const uint32_t u0 = __byte_perm(x[0][q], x[1][q], sel);
-            const uint32_t u1 = __byte_perm(x[2][q], x[3][q], sel);
+            for (int hq = 0; hq < 2; ++hq) {
+              const uint32_t sel = hq ? 0x7362u : 0x5140u;
+              const uint32_t u0 = __byte_perm(x[0][q], x[1][q], sel);
+              const uint32_t u1 = __byte_perm(x[2][q], x[3][q], sel);
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const int n = half * 16 + q * 4 + hq * 2 + o;
-              const uint32_t b0 = o ? e4m3_hi(u0) : e4m3_lo(u0);
-              const uint32_t b1 = o ? e4m3_hi(u1) : e4m3_lo(u1);
-              float a[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(a, pa[0][0], pa[1][0], pa[0][1], pa[1][1], b0, b1);
-              if constexpr (F32) mma_f16(a, pl[0][0], pl[1][0], pl[0][1], pl[1][1], b0, b1);
-#pragma unroll
-              for (int rh = 0; rh < RH; ++rh) {
-                z[rh][n][0] = fmaf(beta[rh], a[2 * rh], z[rh][n][0]);
-                z[rh][n][1] = fmaf(beta[rh], a[2 * rh + 1], z[rh][n][1]);
+              for (int o = 0; o < 2; ++o) {
+                const int n = half * 16 + q * 4 + hq * 2 + o;
+                const uint32_t b0 = o ? e4m3_hi(u0) : e4m3_lo(u0);
+                const uint32_t b1 = o ? e4m3_hi(u1) : e4m3_lo(u1);
+                mma_rows<RH>(z, n, pa, b0, b1);
+                if constexpr (F32) mma_rows<RH>(z, n, pl, b0, b1);
               }
             }
           }
         }
       }
-      if (masked && __any_sync(0xffffffffu, nan)) {
-        for (int key = 0; key < 16; ++key) {
+    }
+    if (masked && __any_sync(0xffffffffu, nan)) {
+      for (int key = 0; key < S::SK; ++key) {
+        if (dead[0] && key < 16) continue;
+        if (S::SUBS == 2 && dead[S::SUBS - 1] && key >= 16) continue;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d = D == 64 ? 8 * (2 * t + e) + n : (n & 16) * 8 + 16 * (2 * t + e) + (n & 15);
-              const uint32_t v = lds8(src + S::ROWS + piece_at<D>(16 * sub + key, d >> 4) + (d & 15));
-              if ((v & 0x7f) != 0x7f) continue;
+          for (int e = 0; e < 2; ++e) {
+            const int d = D == 64 ? 8 * (2 * t + e) + n : (n & 16) * 8 + 16 * (2 * t + e) + (n & 15);
+            const uint32_t v = lds8(src + S::ROWS + piece_at<D>(key, d >> 4) + (d & 15));
+            if ((v & 0x7f) != 0x7f) continue;
 #pragma unroll
-              for (int rh = 0; rh < RH; ++rh)
-                if (kb + key <= limit[rh]) z[rh][n][e] = __int_as_float(0x7fffffff);
-            }
+            for (int rh = 0; rh < RH; ++rh)
+              if (kb + key <= limit[rh]) z[rh][n][e] = __int_as_float(0x7fffffff);
           }
         }
       }
@@ -595,16 +729,16 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int r = rt * 16 + g + 8 * rh;
       if (r >= P.n_q * P.share) continue;
-      const float inv = whole ? (limit[rh] < 0 ? 0.f : 1.f / sum) : 1.f;
-      const bool empty = whole && (limit[rh] < 0 || sum == 0.f);
+      const bool empty = limit[rh] < 0 || sum == 0.f;
+      const float f = 0.0001220703125f * (whole ? 1.f / sum : 1.f);  // 2^-13
       const int i = r / P.share, head = kv * P.share + (r - i * P.share);
       const long long zat = ((long long)cc.b * P.n_q + i) * P.h * P.d_vh + (long long)head * P.d_vh;
       const long long slot = 2ll * w + (start_gi == 0 ? 1 : 0);
       const long long at = slot * P.slot_rows + (g + 8 * rh);
       float* pz = P.part + 2ll * 2 * P.warps * P.slot_rows + at * P.d_vh;
       if (!whole && t == 0) {
-        P.part[2 * at] = m[rh];
-        P.part[2 * at + 1] = sum;
+        P.part[2 * at] = empty ? -INFINITY : m[rh];
+        P.part[2 * at + 1] = empty ? 0.f : sum;
       }
 #pragma unroll
       for (int c = 0; c < COLS; c += 8) {
@@ -620,7 +754,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             n = ((c + k) & 15) + ((c + k) >> 5) * 16;
             e = ((c + k) >> 4) & 1;
           }
-          v[k] = empty ? 0.f : z[rh][n][e] * inv;
+          v[k] = empty ? 0.f : z[rh][n][e] * f * vref;
         }
         const int col = D == 64 ? 16 * t + c : (c >> 5) * 128 + 32 * t + (c & 31);
         if (col >= P.d_vh) continue;
@@ -640,36 +774,34 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
   };
 
-  // fill the ring
-#pragma unroll
-  for (int k = 0; k < S::N - 1; ++k) {
-    if (load_left > 0) {
-      issue(k);
-      advance(lc);
-      --load_left;
-    }
-    cp_async_commit();
-  }
+  // One more group into `stage`, if there is one.
+  auto load_next = [&](int stage) {
+    put_scales();
+    if (load_left <= 0) return;
+    issue(stage);
+    if (--load_left > 0 && advance(lc)) place();
+  };
+#pragma unroll 1
+  for (int k = 0; k < S::N - 1; ++k) load_next(k);
   int stage = 0;
+  uint32_t parity = 0;
+  bool begins = true;
+#pragma unroll 1
   for (; left > 0; --left) {
-    cp_async_wait<S::N - 2>();
-    __syncwarp();  // the stage is filled, and every lane has left the one before
-    if (load_left > 0) {
-      issue(stage == 0 ? S::N - 1 : stage - 1);
-      advance(lc);
-      --load_left;
-    }
-    cp_async_commit();
-    if (piece_starts) begin_tile();
+    __syncwarp();  // every lane has left the stage that is filled now
+    load_next(stage == 0 ? S::N - 1 : stage - 1);
+    if (begins) begin_tile();
+    __syncwarp();  // the scales put by other lanes
+    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity, ctl))) return;
     fold(stage);
-    if (cc.gi == cc.ng - 1 || left == 1) {
-      end_piece();
-      piece_starts = true;
-    }
+    begins = cc.gi == cc.ng - 1 || left == 1;
+    if (begins) end_piece();
     advance(cc);
-    stage = stage == S::N - 1 ? 0 : stage + 1;
+    if (++stage == S::N) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
-  cp_async_wait<0>();
 }
 
 // One output row per CTA: zeros where it sees no key, else the merge of its
@@ -754,6 +886,15 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
 template <int D, int RH, bool F32>
 mha_status launch(CacheAttnParams& P, cudaStream_t s) {
   auto* kernel = cache_attention_kernel<D, RH, F32>;
+  const void* base[2] = {P.K, P.V};
+  CUtensorMap* map[2] = {&P.map_k, &P.map_v};
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t d = i ? P.d_vh : P.d_h;
+    const uint64_t dims[3] = {d, (uint64_t)P.bt, (uint64_t)P.n_blocks * P.h_kv};
+    const uint64_t strides[2] = {d, d * P.bt};
+    const uint32_t box[3] = {Stage<D>::WIDTH, 16, 1};
+    if (!make_tmap_u8(map[i], base[i], 3, dims, strides, box, Stage<D>::WIDTH)) return MHA_ERR_CUDA;
+  }
   if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), Stage<D>::SMEM)) return MHA_ERR_CUDA;
   const int ctas = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
   P.warps = ctas * CA_WARPS;
@@ -811,6 +952,7 @@ mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s)
   P.slot_rows = rows < 16 ? rows : 16;
   P.causal_tail = a.causal_tail;
   P.cl2 = a.c * 1.4426950408889634f;
+  P.limit_ns = wait_limit_ns();
   const int d = a.d_h > a.d_vh ? a.d_h : a.d_vh;
   if (d <= 64) return launch_rows<64>(P, dt, s);
   if (d <= 128) return launch_rows<128>(P, dt, s);

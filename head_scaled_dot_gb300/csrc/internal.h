@@ -209,6 +209,10 @@ mha_status attention_tc_plan(const AttnArgs& a, int num_sms, int* grid, int32_t*
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128);
 
+// As make_tmap_bf16 for bytes; swizzle: 64 or 128 (bytes).
+bool make_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides_bytes, const uint32_t* box, int swizzle);
+
 mha_status selftest_wait(int32_t* err, uint64_t limit_ns, cudaStream_t s);
 
 // Launches kernel(arg) with programmatic stream serialization: it may begin

@@ -97,8 +97,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                    const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
+static bool make_tmap(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, CUtensorMap* map,
+                      const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5], st[4];
@@ -109,11 +110,24 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t
     es[i] = 1;
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
-                  d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
+  return make_tmap(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, map,
+                   base, rank, dims, strides_bytes, box);
+}
+
+bool make_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides_bytes, const uint32_t* box, int swizzle) {
+  return make_tmap(CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                   swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, map,
+                   base, rank, dims, strides_bytes, box);
 }
 
 // ---------------------------------------------------------------------------
@@ -717,9 +731,10 @@ mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V
   if (!dtype_ok(dt) || !isfinite(c)) return MHA_ERR_INVALID_ARG;
   if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > MHA_MAX_PADDED_BATCH)
     return MHA_ERR_UNSUPPORTED;
-  // keys of a sequence, 16-key groups of a batch, output rows: 32-bit counts
+  // keys of a sequence, 16-key groups of a batch, blocks of all heads, output
+  // rows: 32-bit counts
   if (!fits(max_blocks, block_tokens, 1) || !fits(B, max_blocks, block_tokens / 16) ||
-      !fits((long long)B, n_q, h))
+      !fits(n_blocks, h_kv, 1) || !fits((long long)B, n_q, h))
     return MHA_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(Z))
     return MHA_ERR_UNSUPPORTED;

@@ -13,10 +13,10 @@ Bounds. u = 2^-24 is fp32's half step. Each is a worst-case count of roundings:
              for weight, group and merge factors; sums over L keys run in
              steps of 16: (L / 16 + 64) 2 u A; the output's half step.
              fp16's relative step ends at its smallest normal number, 2^-14:
-             weights are scaled by 2^14, so one below 2^-28 of its group's
-             largest is off by up to half of fp16's smallest number, 2^-25,
-             over 2^14. The group's largest weight over the row's sum is at
-             most 1, so that adds up to 2^-39 N, N = sum |v| over the keys
+             weights, of which the row's reference has weight 1, are scaled by
+             at least 2^9 (2^13, less up to 2^4 between blocks' scales), so a
+             small one is off by up to half of fp16's smallest number, 2^-25,
+             over 2^9. That adds up to 2^-34 N, N = sum |v| over the keys
 """
 
 import numpy as np
@@ -389,7 +389,7 @@ def attention_bound(ref, parts, d, longest, dtype):
     weight = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
     score = 2 * (d + 8) * 2 * U * S
     return (HALF_STEP[dtype] * np.abs(ref)
-            + A * (weight + 2 * score + 4 * 2.0 ** -22 + (longest / 16 + 64) * 2 * U) + 2.0 ** -39 * N)
+            + A * (weight + 2 * score + 4 * 2.0 ** -22 + (longest / 16 + 64) * 2 * U) + 2.0 ** -34 * N)
 
 
 def attend_and_check(cache, total, new, n_q, h, d_h, d_vh, dtype, tail, seed, table=None, **kw):
