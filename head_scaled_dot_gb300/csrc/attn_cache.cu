@@ -41,64 +41,16 @@
 //
 // Copies. Each warp keeps a ring of stages of its own (cp.async, 16 bytes per
 // lane), filled ahead of the arithmetic across tile and sequence borders.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
-#include "device_common.cuh"
-#include "internal.h"
+#include "attn_cache.cuh"
 
 namespace mha {
 namespace {
 
-constexpr int CA_WARPS = 8;
 constexpr int CA_THREADS = 32 * CA_WARPS;
-constexpr int CA_MAX_CTAS = 192;   // of the main kernel: bounds the workspace
-constexpr int CA_HEADER = 8192;    // workspace: first group of every batch item
 constexpr int CM_THREADS = 128;    // merge kernel
 
-struct CacheAttnParams {
-  CUtensorMap map_k;    // K as (d_h, bt, n_blocks h_kv) bytes
-  CUtensorMap map_v;
-  const void* Q;        // (B, h, n_q, d_h)
-  const uint8_t* K;     // (n_blocks, h_kv, bt, d_h)
-  const uint8_t* V;     // (n_blocks, h_kv, bt, d_vh)
-  const float* Ks;      // (n_blocks, h_kv)
-  const float* Vs;
-  const int32_t* table; // (B, max_blocks)
-  const int32_t* total; // (B)
-  const int32_t* fresh; // (B) or null: new rows, n_q
-  void* Z;              // (B, n_q, h d_vh)
-  int32_t* first;       // workspace: (B + 1) groups before item b, per tile of rows
-  float* part;          // workspace: summaries, [2 W][slot_rows][2 + d_vh]
-  int32_t* err;
-  int B, n_q, h, h_kv, share, d_h, d_vh, n_blocks, bt, max_blocks;
-  int tiles;            // tiles of 16 rows per key/value head
-  int slot_rows;        // rows of a summary slot: min(16, n_q share)
-  int causal_tail;
-  int warps;            // W
-  float cl2;            // c log2(e)
-  uint64_t limit_ns;    // bounded waits give up after this long
-};
-
-__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* m, uint64_t* bar,
-                                               int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -108,22 +60,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
-}
-
-// Two e4m3 numbers (the low or high half of w) as two fp16 numbers, exactly.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -149,26 +85,10 @@ __device__ __forceinline__ void mma_rows(float (&z)[RH][NT][2], int n, const uin
   }
 }
 
-// Two floats as fp16 (hi), and what that rounding left out as fp16 (lo).
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+// What rounding a and b to fp16 (hi) left out, as fp16.
 __device__ __forceinline__ uint32_t rest_half(float a, float b, uint32_t hi) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   return pack_half(a - f.x, b - f.y);
-}
-
-// The rows of a batch item: keys in the cache and new query rows, each held
-// inside its bounds.
-struct Item {
-  int total, fresh;
-};
-__device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& bad) {
-  const int t = __ldg(P.total + b), f = P.fresh ? __ldg(P.fresh + b) : P.n_q;
-  const int most = P.max_blocks * P.bt;
-  bad = t < 0 || t > most || f < 0 || f > P.n_q;
-  return Item{min(max(t, 0), most), min(max(f, 0), P.n_q)};
 }
 
 // A warp's stage: SK key rows and SK value rows of D bytes, each side as
@@ -214,11 +134,6 @@ __device__ __forceinline__ uint32_t piece_at(int k, int c) {
     return (uint32_t)((c >> 3) * Stage<D>::PLANE + k * 128 + (((c & 7) ^ (k & 7)) << 4));
 }
 
-// Where a warp is in the list of groups.
-struct Cursor {
-  int b, pr, gi, ng;  // batch item, tile of rows in it, group in that, groups per tile
-};
-
 template <int D, int RH, bool F32>
 __global__ void __launch_bounds__(CA_THREADS, 1)
     cache_attention_kernel(const __grid_constant__ CacheAttnParams P) {
@@ -247,82 +162,17 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  // groups per tile of every batch item, and their sums
-  {
-    constexpr int PER = MHA_MAX_PADDED_BATCH / CA_THREADS;
-    int n[PER], sum = 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int b = threadIdx.x * PER + k;
-      n[k] = 0;
-      if (b < P.B) {
-        bool bad;
-        const Item it = item_of(P, b, bad);
-        if (bad && blockIdx.x == 0 && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
-        if (it.fresh > 0) n[k] = (it.total + S::SK - 1) / S::SK;
-      }
-      sum += n[k];
-    }
-    int v = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    int before = v - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int b = threadIdx.x * PER + k;
-      if (b <= P.B) {
-        first[b] = before;
-        if (blockIdx.x == 0) P.first[b] = before;
-      }
-      before += n[k];
-    }
-    if (threadIdx.x == CA_THREADS - 1 && P.B == MHA_MAX_PADDED_BATCH) {
-      first[P.B] = before;
-      if (blockIdx.x == 0) P.first[P.B] = before;
-    }
-    __syncthreads();
-  }
+  scan_groups<CA_THREADS, S::SK>(P, first, warp_sums);
   const int unit = P.h_kv * P.tiles;
   const long long G = (long long)first[P.B] * unit;
   const int w = blockIdx.x * CA_WARPS + warp;
-  const long long g0 = w * G / P.warps;
-  const long long g1 = (w + 1) * G / P.warps;
+  const long long g0 = w * G / P.ranges;
+  const long long g1 = (w + 1) * G / P.ranges;
   if (g0 >= g1) return;
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
-  Cursor cc;  // what is computed
-  {
-    int lo = 0, hi = P.B - 1;  // the last item that starts at or before g0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if ((long long)first[mid] * unit <= g0) lo = mid; else hi = mid - 1;
-    }
-    cc.b = lo;
-    cc.ng = first[lo + 1] - first[lo];
-    const long long in = g0 - (long long)first[lo] * unit;
-    cc.pr = (int)(in / cc.ng);
-    cc.gi = (int)(in - (long long)cc.pr * cc.ng);
-  }
+  Cursor cc = cursor_at(first, P.B, unit, g0);  // what is computed
   int left = (int)(g1 - g0), load_left = left;
-  // true when the cursor has moved to another tile of rows
-  auto advance = [&](Cursor& c) {
-    if (++c.gi < c.ng) return false;
-    c.gi = 0;
-    if (++c.pr < unit) return true;
-    c.pr = 0;
-    do {
-      ++c.b;
-    } while (c.b < P.B && first[c.b + 1] == first[c.b]);
-    c.ng = c.b < P.B ? first[c.b + 1] - first[c.b] : 1;
-    return true;
-  };
-
   const uint32_t ring = smem_u32(smem) + warp * S::N * S::BYTES;
   const uint32_t metas = smem_u32(smem) + S::RING + warp * S::N * S::SUBS * 16;
 
@@ -735,7 +585,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       const long long zat = ((long long)cc.b * P.n_q + i) * P.h * P.d_vh + (long long)head * P.d_vh;
       const long long slot = 2ll * w + (start_gi == 0 ? 1 : 0);
       const long long at = slot * P.slot_rows + (g + 8 * rh);
-      float* pz = P.part + 2ll * 2 * P.warps * P.slot_rows + at * P.d_vh;
+      float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows + at * P.d_vh;
       if (!whole && t == 0) {
         P.part[2 * at] = empty ? -INFINITY : m[rh];
         P.part[2 * at + 1] = empty ? 0.f : sum;
@@ -779,7 +629,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     put_scales();
     if (load_left <= 0) return;
     issue(stage);
-    if (--load_left > 0 && advance(lc)) place();
+    if (--load_left > 0 && advance(lc, first, P.B, unit)) place();
   };
 #pragma unroll 1
   for (int k = 0; k < S::N - 1; ++k) load_next(k);
@@ -792,11 +642,21 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     load_next(stage == 0 ? S::N - 1 : stage - 1);
     if (begins) begin_tile();
     __syncwarp();  // the scales put by other lanes
-    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity, ctl))) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity, ctl))) {
+      // gave up: this warp's copies in flight are waited for before it leaves
+      for (int k = load_left; k < left; ++k) {
+        wait_in_flight(full + stage, parity);
+        if (++stage == S::N) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+      return;
+    }
     fold(stage);
     begins = cc.gi == cc.ng - 1 || left == 1;
     if (begins) end_piece();
-    advance(cc);
+    advance(cc, first, P.B, unit);
     if (++stage == S::N) {
       stage = 0;
       parity ^= 1;
@@ -817,7 +677,7 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
   const long long bi = blockIdx.x / P.h;
   const int i = (int)(bi % P.n_q), b = (int)(bi / P.n_q);
   const int kv = head / P.share, r = i * P.share + head % P.share;
-  const int pr = kv * P.tiles + r / 16, row = r % 16;
+  const int pr = kv * P.tiles + r / P.tile_rows, row = r % P.tile_rows;
   const int unit = P.h_kv * P.tiles;
   const int f0 = P.first[b], ng = P.first[b + 1] - f0;
   const long long G = (long long)P.first[P.B] * unit;
@@ -829,13 +689,13 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
   const Item it = item_of(P, b, bad);
   if (ng > 0) {
     const long long a = (long long)f0 * unit + (long long)pr * ng;
-    const int w0 = (int)(((a + 1) * P.warps - 1) / G), w1 = (int)(((a + ng) * P.warps - 1) / G);
+    const int w0 = (int)(((a + 1) * P.ranges - 1) / G), w1 = (int)(((a + ng) * P.ranges - 1) / G);
     if (w0 == w1) return;
     const float* ml = P.part;
-    const float* pz = P.part + 2ll * 2 * P.warps * P.slot_rows;
+    const float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows;
     for (int w = w0 + pg; w <= w1; w += PG) {
-      const long long s0 = w * G / P.warps;
-      if (s0 == (w + 1) * G / P.warps) continue;  // a warp without work
+      const long long s0 = w * G / P.ranges;
+      if (s0 == (w + 1) * G / P.ranges) continue;  // a warp without work
       const long long at = (2ll * w + (s0 <= a ? 1 : 0)) * P.slot_rows + row;
       const float mw = ml[2 * at], lw = ml[2 * at + 1];
       if (mw == -INFINITY && lw == 0.f) continue;  // the empty summary
@@ -886,41 +746,61 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
 template <int D, int RH, bool F32>
 mha_status launch(CacheAttnParams& P, cudaStream_t s) {
   auto* kernel = cache_attention_kernel<D, RH, F32>;
-  const void* base[2] = {P.K, P.V};
-  CUtensorMap* map[2] = {&P.map_k, &P.map_v};
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t d = i ? P.d_vh : P.d_h;
-    const uint64_t dims[3] = {d, (uint64_t)P.bt, (uint64_t)P.n_blocks * P.h_kv};
-    const uint64_t strides[2] = {d, d * P.bt};
-    const uint32_t box[3] = {Stage<D>::WIDTH, 16, 1};
-    if (!make_tmap_u8(map[i], base[i], 3, dims, strides, box, Stage<D>::WIDTH)) return MHA_ERR_CUDA;
-  }
+  if (!make_cache_maps(P, 16, Stage<D>::WIDTH)) return MHA_ERR_CUDA;
   if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), Stage<D>::SMEM)) return MHA_ERR_CUDA;
   const int ctas = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
-  P.warps = ctas * CA_WARPS;
+  P.ranges = ctas * CA_WARPS;
   cudaError_t e = launch_dependent(kernel, dim3(ctas), dim3(CA_THREADS), Stage<D>::SMEM, s, P);
-  if (e == cudaSuccess) {
-    using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    e = launch_dependent(cache_merge_kernel<D, T>, dim3((unsigned)((long long)P.B * P.n_q * P.h)),
-                         dim3(CM_THREADS), 0, s, P);
-  }
+  if (e == cudaSuccess) e = launch_cache_merge(P, F32 ? MHA_DTYPE_F32 : MHA_DTYPE_BF16, s);
   count_launch(2);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 
-template <int D>
-mha_status launch_rows(CacheAttnParams& P, mha_dtype dt, cudaStream_t s) {
-  const bool two = P.n_q * P.share > 8;
-  if (dt == MHA_DTYPE_F32) return two ? launch<D, 2, true>(P, s) : launch<D, 1, true>(P, s);
-  return two ? launch<D, 2, false>(P, s) : launch<D, 1, false>(P, s);
+template <typename T>
+cudaError_t launch_merge(const CacheAttnParams& P, cudaStream_t s) {
+  const dim3 grid((unsigned)((long long)P.B * P.n_q * P.h)), block(CM_THREADS);
+  if (P.d_vh <= 64) return launch_dependent(cache_merge_kernel<64, T>, grid, block, 0, s, P);
+  if (P.d_vh <= 128) return launch_dependent(cache_merge_kernel<128, T>, grid, block, 0, s, P);
+  return launch_dependent(cache_merge_kernel<256, T>, grid, block, 0, s, P);
+}
+
+// The tensor-core kernel takes bf16 queries and head sizes up to 128: its
+// weights have 8 bits, enough for a bf16 result, and its tiles of 128 keys
+// fill shared memory at 128 columns.
+bool on_tensor_cores(mha_dtype dt, int d_h, int d_vh) {
+  return dt == MHA_DTYPE_BF16 && d_h <= 128 && d_vh <= 128;
 }
 
 }  // namespace
 
-size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_vh) {
+cudaError_t launch_cache_merge(const CacheAttnParams& P, mha_dtype dt, cudaStream_t s) {
+  return dt == MHA_DTYPE_F32 ? launch_merge<float>(P, s) : launch_merge<__nv_bfloat16>(P, s);
+}
+
+bool make_cache_maps(CacheAttnParams& P, int box_rows, int width) {
+  const void* base[2] = {P.K, P.V};
+  CUtensorMap* map[2] = {&P.map_k, &P.map_v};
+  P.box = box_rows;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t d = i ? P.d_vh : P.d_h;
+    const uint64_t dims[3] = {d, (uint64_t)P.bt, (uint64_t)P.n_blocks * P.h_kv};
+    const uint64_t strides[2] = {d, d * P.bt};
+    const uint32_t box[3] = {(uint32_t)width, (uint32_t)box_rows, 1};
+    if (!make_tmap_u8(map[i], base[i], 3, dims, strides, box, width)) return false;
+  }
+  return true;
+}
+
+// A slot per range's first and last tile: the mma.sync kernel has a range per
+// warp and 16 rows a tile, the tensor-core kernel a range per CTA and 16 or
+// 128 rows. The call's element type is not known here: the larger of the two.
+size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_h, int d_vh) {
   const long long rows = (long long)n_q * (h / h_kv);
-  return CA_HEADER + (size_t)2 * CA_MAX_CTAS * CA_WARPS * (rows < 16 ? rows : 16) *
-                         (2 + (size_t)d_vh) * sizeof(float);
+  const size_t few = (size_t)CA_MAX_CTAS * CA_WARPS * (rows < 16 ? rows : 16);
+  const size_t many = (size_t)CA_MAX_CTAS * (rows < 128 ? rows : 128);
+  const size_t slots = 2 * (many > few ? many : few);
+  (void)d_h;
+  return CA_HEADER + slots * (2 + (size_t)d_vh) * sizeof(float);
 }
 
 mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s) {
@@ -947,16 +827,22 @@ mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s)
   P.n_blocks = a.n_blocks;
   P.bt = a.bt;
   P.max_blocks = a.max_blocks;
-  const int rows = a.n_q * P.share;
-  P.tiles = (rows + 15) / 16;
-  P.slot_rows = rows < 16 ? rows : 16;
   P.causal_tail = a.causal_tail;
   P.cl2 = a.c * 1.4426950408889634f;
   P.limit_ns = wait_limit_ns();
+  const int rows = a.n_q * P.share;
+  const bool tc = on_tensor_cores(dt, a.d_h, a.d_vh);
+  // up to 16 rows a tile of 16 (the cache is streamed once), else 128
+  P.tile_rows = tc && rows > 16 ? 128 : 16;
+  P.tiles = (rows + P.tile_rows - 1) / P.tile_rows;
+  P.slot_rows = rows < P.tile_rows ? rows : P.tile_rows;
+  if (tc) return launch_cache_attention_tc(P, s);
   const int d = a.d_h > a.d_vh ? a.d_h : a.d_vh;
-  if (d <= 64) return launch_rows<64>(P, dt, s);
-  if (d <= 128) return launch_rows<128>(P, dt, s);
-  return launch_rows<256>(P, dt, s);
+  const bool two = rows > 8;
+  if (dt == MHA_DTYPE_BF16) return two ? launch<256, 2, false>(P, s) : launch<256, 1, false>(P, s);
+  if (d <= 64) return two ? launch<64, 2, true>(P, s) : launch<64, 1, true>(P, s);
+  if (d <= 128) return two ? launch<128, 2, true>(P, s) : launch<128, 1, true>(P, s);
+  return two ? launch<256, 2, true>(P, s) : launch<256, 1, true>(P, s);
 }
 
 }  // namespace mha

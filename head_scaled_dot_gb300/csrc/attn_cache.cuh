@@ -1,0 +1,196 @@
+// attn_cache.cuh - what the kernels of the attention over the 8-bit cache
+// share: parameters, the list of groups that is cut into equal ranges, TMA.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+
+namespace mha {
+
+constexpr int CA_MAX_CTAS = 192;   // of the main kernels: bounds the workspace
+constexpr int CA_WARPS = 8;        // warps of the mma.sync kernel, a range each
+constexpr int CA_HEADER = 8192;    // workspace: first group of every batch item
+
+struct CacheAttnParams {
+  CUtensorMap map_k;    // K as (d_h, bt, n_blocks h_kv) bytes
+  CUtensorMap map_v;
+  const void* Q;        // (B, h, n_q, d_h)
+  const uint8_t* K;     // (n_blocks, h_kv, bt, d_h)
+  const uint8_t* V;     // (n_blocks, h_kv, bt, d_vh)
+  const float* Ks;      // (n_blocks, h_kv)
+  const float* Vs;
+  const int32_t* table; // (B, max_blocks)
+  const int32_t* total; // (B)
+  const int32_t* fresh; // (B) or null: new rows, n_q
+  void* Z;              // (B, n_q, h d_vh)
+  int32_t* first;       // workspace: (B + 1) groups before item b, per tile of rows
+  float* part;          // workspace: summaries, [2 ranges][slot_rows][2], then [2 ranges][slot_rows][d_vh]
+  int32_t* err;
+  int B, n_q, h, h_kv, share, d_h, d_vh, n_blocks, bt, max_blocks;
+  int tile_rows;        // query rows per tile: row r is new row r / share of head r % share
+  int tiles;            // tiles per key/value head
+  int slot_rows;        // rows of a summary slot
+  int box;              // rows per TMA box
+  int causal_tail;
+  int ranges;           // the list of groups is cut into so many equal ranges
+  float cl2;            // c log2(e)
+  uint64_t limit_ns;    // bounded waits give up after this long
+};
+
+// Merges the summaries of the tiles that more than one range had a part of,
+// and writes the rows that see no key (attn_cache.cu).
+cudaError_t launch_cache_merge(const CacheAttnParams& P, mha_dtype dt, cudaStream_t s);
+// Tensor-core kernel for bf16 queries and head sizes up to 128 (attn_cache_tc.cu).
+mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s);
+// The tensor maps of the cache, for boxes of `box` rows of `width` bytes.
+bool make_cache_maps(CacheAttnParams& P, int box, int width);
+
+// The rows of a batch item: keys in the cache and new query rows, each held
+// inside its bounds.
+struct Item {
+  int total, fresh;
+};
+__device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& bad) {
+  const int t = __ldg(P.total + b), f = P.fresh ? __ldg(P.fresh + b) : P.n_q;
+  const int most = P.max_blocks * P.bt;
+  bad = t < 0 || t > most || f < 0 || f > P.n_q;
+  return Item{min(max(t, 0), most), min(max(f, 0), P.n_q)};
+}
+
+// first[b], b = 0 .. B: groups of SK keys per tile of rows before batch item
+// b. Every CTA computes them; the first one leaves them in the workspace and
+// reports lengths out of bounds. All threads of the CTA.
+template <int THREADS, int SK>
+__device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first, int* warp_sums) {
+  constexpr int PER = (MHA_MAX_PADDED_BATCH + THREADS - 1) / THREADS;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int n[PER], sum = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int b = threadIdx.x * PER + k;
+    n[k] = 0;
+    if (b < P.B) {
+      bool bad;
+      const Item it = item_of(P, b, bad);
+      if (bad && blockIdx.x == 0 && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+      if (it.fresh > 0) n[k] = (it.total + SK - 1) / SK;
+    }
+    sum += n[k];
+  }
+  int v = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int before = v - sum;
+  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int b = threadIdx.x * PER + k;
+    if (b <= P.B) {
+      first[b] = before;
+      if (blockIdx.x == 0) P.first[b] = before;
+    }
+    before += n[k];
+  }
+  if (threadIdx.x == THREADS - 1 && P.B == THREADS * PER) {
+    first[P.B] = before;
+    if (blockIdx.x == 0) P.first[P.B] = before;
+  }
+  __syncthreads();
+}
+
+// A place in the list of groups: batch item by batch item, in it tile by tile
+// (tile `pr` = key/value head * tiles + tile of rows), in that group by group.
+struct Cursor {
+  int b, pr, gi, ng;  // ng: groups per tile of this item
+};
+__device__ __forceinline__ Cursor cursor_at(const int* first, int B, int unit, long long g) {
+  int lo = 0, hi = B - 1;  // the last item that starts at or before g
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if ((long long)first[mid] * unit <= g) lo = mid; else hi = mid - 1;
+  }
+  Cursor c;
+  c.b = lo;
+  c.ng = first[lo + 1] - first[lo];
+  const long long in = g - (long long)first[lo] * unit;
+  c.pr = (int)(in / c.ng);
+  c.gi = (int)(in - (long long)c.pr * c.ng);
+  return c;
+}
+// True when the cursor has moved to another tile.
+__device__ __forceinline__ bool advance(Cursor& c, const int* first, int B, int unit) {
+  if (++c.gi < c.ng) return false;
+  c.gi = 0;
+  if (++c.pr < unit) return true;
+  c.pr = 0;
+  do {
+    ++c.b;
+  } while (c.b < B && first[c.b + 1] == first[c.b]);
+  c.ng = c.b < B ? first[c.b + 1] - first[c.b] : 1;
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* m, uint64_t* bar,
+                                               int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Waits, with a limit of its own, until a barrier phase has completed although
+// a wait has been given up: for copies or products still in flight.
+static __device__ __noinline__ void wait_in_flight(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1; it != 0; ++it) {
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return;
+    if (globaltimer_ns() - t0 > 100000000ull) return;
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// Two e4m3 numbers (the low or high half of w) as two fp16 numbers, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+// Two floats as fp16.
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace mha

@@ -153,13 +153,15 @@ def cache_rows(codes, scale, blocks, total, head, block_tokens):
 def attention_cache(Q, K_codes, V_codes, K_scale, V_scale, table, total, new, c, causal_tail):
     """Z (B, n_q, h d_vh), and a tuple of what error bounds are made of, each of
     Z's shape: A, the same sums with |v| for v; S, per row, the largest
-    c sum |q| |k|; N, the sums of |v| over the keys seen, without weights."""
+    c sum |q| |k|; N, the sums of |v| over the keys seen, without weights; T, per
+    row, the largest c max |q| sum |k|."""
     B, h, n_q, _ = Q.shape
     h_kv, bt, d_vh = V_codes.shape[1], V_codes.shape[2], V_codes.shape[3]
     Z = np.zeros((B, n_q, h, d_vh))
     A = np.zeros((B, n_q, h, d_vh))
     S = np.zeros((B, n_q, h, 1))
     N = np.zeros((B, n_q, h, d_vh))
+    T = np.zeros((B, n_q, h, 1))
     for b in range(B):
         for kv in range(h_kv):
             if total[b] <= 0 or new[b] <= 0:
@@ -179,5 +181,7 @@ def attention_cache(Q, K_codes, V_codes, K_scale, V_scale, table, total, new, c,
                     A[b, i, j] = p @ np.abs(V[:seen])
                     N[b, i, j] = np.abs(V[:seen]).sum(axis=0)
                     S[b, i, j] = abs(c) * (np.abs(K[:seen]) @ np.abs(q)).max()
+                    T[b, i, j] = abs(c) * np.abs(q).max() * np.abs(K[:seen]).sum(axis=1).max()
     flat = lambda x: x.reshape(B, n_q, -1)
-    return flat(Z), (flat(A), flat(np.repeat(S, d_vh, axis=3)), flat(N))
+    wide = lambda x: flat(np.repeat(x, d_vh, axis=3))
+    return flat(Z), (flat(A), wide(S), flat(N), wide(T))

@@ -95,7 +95,7 @@ def test_append_then_attention_is_dense_attention_of_the_rounded_rows():
         return y
     Q = g.normal(size=(B, h, 3, d))
     for tail in (False, True):
-        Z, (A, _, _) = co.attention_cache(Q, codes[0], codes[1], scale[0], scale[1], table, [n, n],
+        Z, (A, _, _, _) = co.attention_cache(Q, codes[0], codes[1], scale[0], scale[1], table, [n, n],
                                      [3, 3], 0.25, tail)
         ref = oracle.attention_decode(Q, rounded(K), rounded(V), 0.25, [n, n], tail)
         assert np.allclose(Z, ref, atol=1e-12)

@@ -6,17 +6,24 @@ Bounds. u = 2^-24 is fp32's half step. Each is a worst-case count of roundings:
              u/2 of a half turn, so pi u/2 radians), sine and cosine within 2
              units (4 u), two products and a sum: |a| + |b| times 8 u, and the
              output's own half step for bf16 (2^-8)
-  attention  with A = sum p |v| and s = max c sum |q| |k|: a score is off by at
-             most (d + 8) 2 u s (sums in tensor cores keep at least 23 bits:
-             2 u a step), and shifts every weight by twice that; weights are
-             rounded to fp16 (2^-11; 2^-22 in fp32 mode), ex2 to 2^-22 each
-             for weight, group and merge factors; sums over L keys run in
-             steps of 16: (L / 16 + 64) 2 u A; the output's half step.
-             fp16's relative step ends at its smallest normal number, 2^-14:
-             weights, of which the row's reference has weight 1, are scaled by
-             at least 2^9 (2^13, less up to 2^4 between blocks' scales), so a
-             small one is off by up to half of fp16's smallest number, 2^-25,
-             over 2^9. That adds up to 2^-34 N, N = sum |v| over the keys
+  attention  with A = sum p |v|, N = sum |v| over the keys, S = max c sum |q| |k|
+             and T = max c max |q| sum |k|:
+             a score is off by at most (d + 8) 2 u S (sums in tensor cores
+             keep at least 23 bits: 2 u a step), and shifts every weight by
+             twice that; ex2 is off by 2^-22 for each weight, group and merge
+             factor; sums over L keys run in steps of 16: (L / 16 + 64) 2 u A;
+             the output's half step. Weights are rounded, the row's reference
+             having weight 1, and small ones to the smallest number's half:
+             fp32 queries, bf16 ones of more than 128 columns: two fp16 or one,
+               2^-22 or 2^-11; scaled by at least 2^9 (2^13, less up to 2^4
+               between blocks' scales), so 2^-25 / 2^9 = 2^-34 N;
+             other bf16 queries: fp16, then hi + lo / 16 in e4m3, 2^-11 and the
+               2^-4 of hi times that of lo, 2^-8; scaled by at least 2^4 (2^8
+               less 2^4), lo's smallest half is 2^-10 / 2^4, so 2^-18 N.
+               Their query elements are hi + lo / 16 of a row whose largest is
+               at least 2^7, exact but for lo's smallest half, 2^-14 of it,
+               2^-21 T on a score; with more than 16 rows per key/value head lo
+               is not scaled: 2^-10 / 2^7 = 2^-17 T
 """
 
 import numpy as np
@@ -384,12 +391,17 @@ def table_of(total, bt, n_blocks, max_blocks, seed, fill=-1):
     return table
 
 
-def attention_bound(ref, parts, d, longest, dtype):
-    A, S, N = parts
-    weight = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
-    score = 2 * (d + 8) * 2 * U * S
-    return (HALF_STEP[dtype] * np.abs(ref)
-            + A * (weight + 2 * score + 4 * 2.0 ** -22 + (longest / 16 + 64) * 2 * U) + 2.0 ** -34 * N)
+def attention_bound(ref, parts, d, longest, dtype, rows=1):
+    """d: the larger head size; rows: query rows per key/value head."""
+    A, S, N, T = parts
+    score = (d + 8) * 2 * U * S
+    if dtype == "bf16" and d <= 128:
+        weight, floor = 2.0 ** -8 + 2.0 ** -11, 2.0 ** -18
+        score = score + T * (2.0 ** -21 if rows <= 16 else 2.0 ** -17)
+    else:
+        weight, floor = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22, 2.0 ** -34
+    return (HALF_STEP[dtype] * np.abs(ref) + floor * N
+            + A * (weight + 2 * 2 * score + 4 * 2.0 ** -22 + (longest / 16 + 64) * 2 * U))
 
 
 def attend_and_check(cache, total, new, n_q, h, d_h, d_vh, dtype, tail, seed, table=None, **kw):
@@ -406,7 +418,7 @@ def attend_and_check(cache, total, new, n_q, h, d_h, d_vh, dtype, tail, seed, ta
     assert mha.get_device_error(err) == OK
     ref, parts = co.attention_cache(f64(Q), cache.o["K"], cache.o["V"], cache.o["Ks"],
                                    cache.o["Vs"], table, total, new or [n_q] * B, c, tail)
-    tol = attention_bound(ref, parts, d_h, max(total), dtype)
+    tol = attention_bound(ref, parts, max(d_h, d_vh), max(total), dtype, n_q * h // cache.t["K"].shape[1])
     got = f64(Z)
     assert np.isfinite(got).all()
     assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
@@ -645,7 +657,7 @@ def test_prompt_and_generation_steps_through_the_whole_chain(graph):
         cache.check()
         ref, parts = co.attention_cache(f64(Qr), cache.o["K"], cache.o["V"], cache.o["Ks"],
                                        cache.o["Vs"], want[3], want[0], new, c, True)
-        assert (np.abs(f64(Z) - ref) <= attention_bound(ref, parts, d, max(want[0]), "bf16")).all()
+        assert (np.abs(f64(Z) - ref) <= attention_bound(ref, parts, d, max(want[0]), "bf16", n)).all()
         y = f64(Z) @ f64(W_O)
         size = np.abs(f64(Z)) @ np.abs(f64(W_O))
         assert (np.abs(f64(Y) - y) <= HALF_STEP["bf16"] * np.abs(y) + 512 * U * size).all()
