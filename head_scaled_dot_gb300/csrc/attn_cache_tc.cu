@@ -20,8 +20,7 @@
 //     tensor-memory lanes of one warp each) all hold the same 16 rows, hi in
 //     the first 16 lanes and lo in the others; warp q takes keys 32 q ..
 //     32 q + 31 of a tile from its own lanes, keeps its own summary (m, l, z)
-//     of them, and its weights of the other keys are zeros in shared memory.
-//     So four warps share a tile of 16 rows without ever meeting, until the
+//     of them, and writes zeros as its weights of the other keys. So four warps share a tile of 16 rows without ever meeting, until the
 //     four summaries are merged at the end.
 //   wide, 128 rows, one per lane: hi and lo of the queries go into the same
 //     accumulator (lo is not scaled there: exact down to 2^-9 of the largest
@@ -34,9 +33,10 @@
 // beside the softmax step of eight warps.
 //
 // Pipeline of a CTA (one per SM, persistent over its range of the list of
-// groups): warp 0 fills the ring of stages, warp 1 issues the products (the
-// scores of the next group before the value product of the current one), the
-// softmax warps turn scores into weights. z stays in tensor memory; it is
+// groups): warps 0, 2 and 3 fill the ring of stages, warp 1 issues the
+// products (the scores of the next group before the value product of the
+// current one), the softmax warps turn scores into weights, which go over the scores in tensor
+// memory as the value product's other operand. z stays in tensor memory; it is
 // rescaled only where a row's reference is raised or the values' scale moves.
 //
 // Measured against the mma.sync kernel of attn_cache.cu, which this one
@@ -54,7 +54,7 @@ constexpr int STAGE = 2 * SIDE;
 constexpr int STAGES = 4;
 constexpr int OPERAND = 128 * ROW;      // 128 operand rows of e4m3
 constexpr int TMEM_COLS = 512;
-constexpr int S_COL = 0;                // two score tiles of 128 columns
+constexpr int S_COL = 0;                // two score tiles of 128 columns; the weights over them
 constexpr int Z_COL = 256;              // z; wide: hi, and lo at Z_COL + 128
 constexpr float RAISE = 0.75f;          // p at most 2^0.75 (448 = 1.75 2^8)
 
@@ -77,8 +77,7 @@ struct Form {
   static constexpr int SUBS = WIDE ? 4 : 1;        // groups of 16 keys per lane
   // shared memory
   static constexpr int Q_AT = STAGES * STAGE;
-  static constexpr int P_AT = Q_AT + PIECES * OPERAND;
-  static constexpr int M_AT = P_AT + PIECES * OPERAND;      // narrow: four summaries' z
+  static constexpr int M_AT = Q_AT + PIECES * OPERAND;      // narrow: four summaries' z
   static constexpr int META_AT = M_AT + (WIDE ? 0 : 4 * 16 * 128 * 4);
   static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
   static constexpr int LIM_AT = NAN_AT + ROWS * 16;
@@ -100,6 +99,17 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
+// The same with A in tensor memory, four elements per column.
+__device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor of kind f8f6f4: e4m3 A (K-major) and B, fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -117,6 +127,32 @@ __device__ __forceinline__ void tmem_ld_x2_16(uint32_t taddr, uint32_t (&r)[16])
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr), "n"(OFF));
+}
+
+// Half-split stores: lane i < 16 to the columns from taddr on of TMEM lane i,
+// lane i + 16 to those at OFF of the same TMEM lane.
+template <int OFF>
+__device__ __forceinline__ void tmem_st_x2_4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2, %3, %4, %5};" ::"r"(taddr),
+               "n"(OFF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void tmem_st_x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17};" ::"r"(taddr),
+      "n"(OFF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Zeros in eight columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_zero8(uint32_t taddr) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(
+                   taddr),
+               "r"(0)
+               : "memory");
 }
 
 __device__ __forceinline__ void fence_async_shared() {
@@ -185,8 +221,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [STAGES] tiles and scales there
   uint64_t* empty = full + STAGES;    // [STAGES] both products done
   uint64_t* s_full = empty + STAGES;  // [2] scores there
-  uint64_t* s_free = s_full + 2;      // [2] scores read
-  uint64_t* q_full = s_free + 2;      // the tile's queries there
+  uint64_t* q_full = s_full + 2;      // the tile's queries there
   uint64_t* p_full = q_full + 1;      // weights there
   uint64_t* p_free = p_full + 1;      // value product done
   uint64_t* done = p_free + 1;
@@ -197,13 +232,10 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full + s, 2);
+      mbar_init(full + s, 3);  // key tiles, value tiles, scales
       mbar_init(empty + s, 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(s_full + s, 1);
-      mbar_init(s_free + s, F::SOFTMAX_WARPS);
-    }
+    for (int s = 0; s < 2; ++s) mbar_init(s_full + s, 1);
     mbar_init(q_full, F::SOFTMAX_WARPS);
     mbar_init(p_full, F::SOFTMAX_WARPS);
     mbar_init(p_free, 1);
@@ -216,11 +248,6 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
-  }
-  if (!WIDE) {  // the weights of the other warps' keys
-    for (int e = threadIdx.x; e < OPERAND / 16; e += F::THREADS)
-      reinterpret_cast<uint4*>(smem + F::P_AT)[e] = make_uint4(0u, 0u, 0u, 0u);
-    fence_async_shared();
   }
   tc_fence_before();
   __syncthreads();
@@ -237,100 +264,96 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
   const int steps = (int)(g1 - g0);
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
-  if (steps > 0 && warp == 0) {
-    // ---- the ring ----
+  if (steps > 0 && warp < 4 && warp != 1) {
+    // ---- the ring: warp 0 the key tiles, warp 2 the value tiles, warp 3 the
+    // scales, each walking the groups for itself ----
+    // A lane has one box of a tile (warp 3: 16 keys of it): its entry j of the
+    // block table and its row in that block, moved on by 128 keys a step.
+    // Entries come from two windows of 32, the second asked for ahead of use.
+    const int span = warp == 3 ? 16 : P.box;
+    const bool mine = lane < KEYS / span;
+    const int dj = KEYS / P.bt, drow = KEYS % P.bt;
     Cursor lc = cursor_at(first, P.B, unit, g0);
-    int lj, lrow, lkv, ltotal, win, win_id, next_id;  // place in the block table, two windows of it
-    auto table_entry = [&](int j) {
-      return j < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + j) : -1;
+    int j, row, kv, total, win, win_id, next_id;
+    auto table_entry = [&](int i) {
+      return i < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + i) : -1;
     };
     auto place = [&]() {
       bool bad;
-      const int k0 = lc.gi * KEYS;
-      ltotal = item_of(P, lc.b, bad).total;
-      lkv = lc.pr / P.tiles;
-      lj = k0 / P.bt;
-      lrow = k0 - lj * P.bt;
-      win = lj;
+      const int k = lc.gi * KEYS + (mine ? lane * span : 0);
+      total = item_of(P, lc.b, bad).total;
+      kv = lc.pr / P.tiles;
+      j = k / P.bt;
+      row = k - j * P.bt;
+      win = __shfl_sync(0xffffffffu, j, 0);
       win_id = table_entry(win + lane);
       next_id = table_entry(win + 32 + lane);
     };
     place();
-    const int boxes = KEYS / P.box;
-    float hks = 0.f, hvs = 0.f;
-    bool hfound = false;
-    int held = -1;  // stage whose scales are on their way
-    auto put_scales = [&]() {
-      if (held < 0) return;
-      Meta* m = metas + held;
-      const uint32_t found = __ballot_sync(0xffffffffu, lane < 8 && hfound);
-      float top = hfound ? hvs : 0.f, least = hfound ? hvs : 3.4e38f;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-      }
-      if (lane < 8) {
-        m->ks[lane] = hks;
-        m->vs[lane] = hvs;
-      }
-      if (lane == 0) {
-        m->found = found;
-        m->top = top;
-        m->single = !(least < 0.25f * top);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + held);
-      held = -1;
-    };
+    const CUtensorMap* map = warp == 0 ? &P.map_k : &P.map_v;
+    const uint32_t tiles = smem_u32(smem) + (warp == 0 ? 0 : SIDE) + lane * span * ROW;
     bool ok = true;
     int n = 0;
     for (; n < steps; ++n) {
       const int stage = n % STAGES;
-      if (n >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, (n / STAGES - 1) & 1, ctl));
-      if (!ok) break;
-      if (lj + 8 >= win + 32) {  // lane i takes entry lj + i of the two windows
-        const int at = lane + lj - win;
+      const int j0 = __shfl_sync(0xffffffffu, j, 0);
+      if (j0 + 8 >= win + 32) {  // lane i takes entry j0 + i of the two windows
+        const int at = lane + j0 - win;
         const int x = __shfl_sync(0xffffffffu, win_id, at & 31);
         const int y = __shfl_sync(0xffffffffu, next_id, at & 31);
         win_id = at < 32 ? x : y;
-        win = lj;
+        win = j0;
         next_id = table_entry(win + 32 + lane);
       }
-      const int k0 = lc.gi * KEYS;
-      const bool in = lane < boxes;
-      int x = lrow + (in ? lane * P.box : 0);
-      const int bj = lj + x / P.bt, brow = x % P.bt;
-      int id = __shfl_sync(0xffffffffu, win_id, bj - win);
-      const bool used = in && k0 + lane * P.box < ltotal;
+      const int id = __shfl_sync(0xffffffffu, win_id, j - win);
+      const bool used = mine && lc.gi * KEYS + lane * span < total;
       const bool there = used && id >= 0 && id < P.n_blocks;
-      if (used && !there && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
-      const uint32_t load = __ballot_sync(0xffffffffu, there);
-      if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(load) * P.box * 2 * ROW);
-      __syncwarp();
-      if (there) {
-        const uint32_t dst = smem_u32(smem) + stage * STAGE + lane * P.box * ROW;
-        tma_load_3d_at(dst, &P.map_k, full + stage, 0, brow, id * P.h_kv + lkv);
-        tma_load_3d_at(dst + SIDE, &P.map_v, full + stage, 0, brow, id * P.h_kv + lkv);
+      const int blk = id * P.h_kv + kv;
+      if (warp == 3) {
+        // the scales are on their way while the stage is waited for
+        const float ks = there ? __ldg(P.Ks + blk) : 0.f, vs = there ? __ldg(P.Vs + blk) : 0.f;
+        const uint32_t found = __ballot_sync(0xffffffffu, there);
+        if (n >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, (n / STAGES - 1) & 1, ctl));
+        if (!ok) break;
+        float top = there ? vs : 0.f, least = there ? vs : 3.4e38f;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+        }
+        Meta* m = metas + stage;
+        if (mine) {
+          m->ks[lane] = ks;
+          m->vs[lane] = vs;
+        }
+        if (lane == 0) {
+          m->found = found;
+          m->top = top;
+          m->single = !(least < 0.25f * top);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + stage);
+      } else {
+        if (used && !there && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+        const uint32_t load = __ballot_sync(0xffffffffu, there);
+        if (n >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, (n / STAGES - 1) & 1, ctl));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(load) * span * ROW);
+        __syncwarp();
+        if (there) tma_load_3d_at(tiles + stage * STAGE, map, full + stage, 0, row, blk);
       }
-      x = lrow + (lane & 7) * 16;
-      id = __shfl_sync(0xffffffffu, win_id, lj + x / P.bt - win);
-      const bool found = k0 + (lane & 7) * 16 < ltotal && id >= 0 && id < P.n_blocks;
-      put_scales();
-      hfound = found;
-      hks = found ? __ldg(P.Ks + (long long)id * P.h_kv + lkv) : 0.f;
-      hvs = found ? __ldg(P.Vs + (long long)id * P.h_kv + lkv) : 0.f;
-      held = stage;
       if (advance(lc, first, P.B, unit)) {
         if (n + 1 < steps) place();
       } else {
-        lrow += KEYS;
-        lj += lrow / P.bt;
-        lrow %= P.bt;
+        j += dj;
+        row += drow;
+        if (row >= P.bt) {
+          row -= P.bt;
+          ++j;
+        }
       }
     }
-    put_scales();
-    if (!ok)  // gave up: the copies in flight are waited for before the CTA ends
+    if (!ok && warp != 3)  // gave up: the copies in flight are waited for before the CTA ends
       for (int k = n > STAGES ? n - STAGES : 0; k < n; ++k)
         wait_in_flight(full + k % STAGES, (k / STAGES) & 1);
   } else if (steps > 0 && warp == 1 && lane == 0) {
@@ -340,7 +363,6 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
     const int slices = (P.d_h + 31) / 32;
     const uint32_t base = smem_u32(smem);
     const uint64_t q_desc = sdesc_sw128(base + F::Q_AT, 16, 1024);
-    const uint64_t p_desc = sdesc_sw128(base + F::P_AT, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(base, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(base + SIDE, 16384, 1024);
     Cursor cc = cursor_at(first, P.B, unit, g0);
@@ -348,8 +370,9 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
     int tile = 0, pv = 0;
     auto issue_s = [&](int n) {
       const int stage = n % STAGES, b = n & 1;
+      // The scores go over the weights of group n - 2, whose value product is
+      // ahead of them in this thread's order.
       ok = ok && mbar_wait(full + stage, (n / STAGES) & 1, ctl);
-      if (n >= 2) ok = ok && mbar_wait(s_free + b, ((n >> 1) - 1) & 1, ctl);
       if (!ok) return;
       tc_fence_after();
       const uint64_t kd = k_desc + (uint64_t)(stage * STAGE >> 4);
@@ -389,8 +412,8 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
         for (int p = 0; p < F::PIECES; ++p) {
 #pragma unroll
           for (int k = 0; k < KEYS / 32; ++k)
-            umma_f8(tmem + Z_COL + p * 128, p_desc + (uint64_t)((p * OPERAND + k * 32) >> 4),
-                    vd + (uint64_t)(k * 32 * ROW >> 4), idesc_z, !fresh || k > 0);
+            umma_f8_ts(tmem + Z_COL + p * 128, tmem + S_COL + (n & 1) * KEYS + p * 32 + k * 8,
+                       vd + (uint64_t)(k * 32 * ROW >> 4), idesc_z, !fresh || k > 0);
         }
         umma_commit(p_free);
         fresh = false;
@@ -415,7 +438,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
     uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
     int* lim_s = reinterpret_cast<int*>(smem + F::LIM_AT);
     float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
-    const uint32_t q_base = smem_u32(smem) + F::Q_AT, p_base = smem_u32(smem) + F::P_AT;
+    const uint32_t q_base = smem_u32(smem) + F::Q_AT;
     Cursor cc = cursor_at(first, P.B, unit, g0);
     bool ok = true, begins = true;
     int pv = 0, start_gi = 0;
@@ -560,9 +583,6 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
             for (int k = 0; k < 16; ++k)
               s[0][k] = fmaf(__uint_as_float(y[k]), 0.0625f, __uint_as_float(x[k]));
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free + b);
         }
         const int sub0 = WIDE ? 4 * half : 2 * q + half;  // this lane's groups of 16 keys
         float mx = -INFINITY;
@@ -626,6 +646,8 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
         // that z cannot overflow. Blocks further apart go one after another.
         uint32_t todo = meta->single ? 0u : found;
         bool fresh = begins;  // z holds nothing yet
+        bool again = false;   // a further round
+        const uint32_t p_at = tmem + lanes + S_COL + b * KEYS;
         do {
           float top = meta->top;
           uint32_t take = found;
@@ -641,32 +663,41 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
             if (seen > 0.f) by = vref / to;
             vref = to;
           }
-          if (pv > 0) ok = __all_sync(0xffffffffu, mbar_wait(p_free, (pv - 1) & 1, ctl));
-          if (!ok) break;
+          // z may be changed, and weights of this group replaced, only behind
+          // the products so far (all but the last one are: the scores of this
+          // group came after them)
           const float f = alpha * by;
-          if (__any_sync(0xffffffffu, f != 1.f) && !fresh) scale_z(f);
+          const bool scales = !fresh && __any_sync(0xffffffffu, f != 1.f);
+          if (scales || again) {
+            ok = __all_sync(0xffffffffu, mbar_wait(p_free, (pv - 1) & 1, ctl));
+            if (!ok) break;
+            if (scales) scale_z(f);
+          }
           alpha = 1.f;
           fresh = false;
+          again = true;
+          uint32_t hi[4 * F::SUBS], lo[4 * F::SUBS];
 #pragma unroll
           for (int i = 0; i < F::SUBS; ++i) {
-            const int sub = sub0 + i;
-            const float r = take >> sub & 1 ? 256.f * (meta->vs[sub] / vref) : 0.f;
-            uint32_t hi[4], lo[4];
+            const float r = take >> (sub0 + i) & 1 ? 256.f * (meta->vs[sub0 + i] / vref) : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               split4<4>(s[i][4 * k] * r, s[i][4 * k + 1] * r, s[i][4 * k + 2] * r, s[i][4 * k + 3] * r,
-                        hi[k], lo[k]);
-            const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if constexpr (WIDE) {
-              sts128(p_base + swz(row, sub), h4);
-              sts128(p_base + OPERAND + swz(row, sub), l4);
-            } else {
-              sts128(p_base + swz(32 * q + row, sub), h4);
-              sts128(p_base + swz(32 * q + 16 + row, sub), l4);
-            }
+                        hi[4 * i + k], lo[4 * i + k]);
           }
-          fence_async_shared();
+          if constexpr (WIDE) {
+            tmem_st_x2_16<16>(p_at, hi);
+            tmem_st_x2_16<16>(p_at + 32, lo);
+          } else {
+            tmem_st_x2_4<4>(p_at + 8 * q, hi);
+            tmem_st_x2_4<4>(p_at + 8 * q + lo_lanes, lo);
+            // no weight for the other warps' keys
+            tmem_zero8(p_at + ((8 * q + 8) & 31));
+            tmem_zero8(p_at + ((8 * q + 16) & 31));
+            tmem_zero8(p_at + ((8 * q + 24) & 31));
+          }
+          tmem_wait_st();
+          if (masked) fence_async_shared();  // value rows may have been mended
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full);
