@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     load_next(stage == 0 ? S::N - 1 : stage - 1);
     if (begins) begin_tile();
     __syncwarp();  // the scales put by other lanes
-    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity, ctl))) {
+    if (!__all_sync(0xffffffffu, cache_wait(full + stage, parity, ctl))) {
       // gave up: this warp's copies in flight are waited for before it leaves
       for (int k = load_left; k < left; ++k) {
         wait_in_flight(full + stage, parity);

@@ -147,6 +147,20 @@ __device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+// The bounded wait with everything but the first look out of line: a kernel
+// whose warps have different roles waits in many places, and its code has to
+// stay in the instruction cache (with the whole wait in each place, the
+// tensor-core kernels were 80 to 170 KB long and stalled on fetching it). Once
+// any wait of the CTA has given up, all others return at once.
+static __device__ __noinline__ bool cache_wait_slow(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (*w.abort) return false;
+  return mbar_wait_slow(bar, parity, w);
+}
+__device__ __forceinline__ bool cache_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return cache_wait_slow(bar, parity, w);
+}
+
 // Waits, with a limit of its own, until a barrier phase has completed although
 // a wait has been given up: for copies or products still in flight.
 static __device__ __noinline__ void wait_in_flight(uint64_t* bar, uint32_t parity) {

@@ -11,37 +11,33 @@
 //            lo, down to 2^-13 of the row's largest element.
 //   weights  p = 2^{s - m}, times 2^8 vs / vref: 8 bits, down to 2^-18 of the
 //            weight of the row's reference m.
-// Each hi and lo is an operand row of its own, so the sums are exact fp32
-// additions of the two accumulator rows.
 //
-// Two forms, by the rows of a tile (new rows times the query heads that share
-// a key/value head):
-//   narrow, 16 rows. An MMA has 128 operand rows. Its four groups of 32 (the
-//     tensor-memory lanes of one warp each) all hold the same 16 rows, hi in
-//     the first 16 lanes and lo in the others; warp q takes keys 32 q ..
-//     32 q + 31 of a tile from its own lanes, keeps its own summary (m, l, z)
-//     of them, and writes zeros as its weights of the other keys. So four warps share a tile of 16 rows without ever meeting, until the
-//     four summaries are merged at the end.
-//   wide, 128 rows, one per lane: hi and lo of the queries go into the same
-//     accumulator (lo is not scaled there: exact down to 2^-9 of the largest
-//     element, off by at most 2^-17 of it below), those of the weights into
-//     two.
-//
-// Bound. Narrow: reading the cache. One 32 KB stage takes about 1500 cycles of
-// its SM's share of HBM, 540 of tensor work and 500 of its softmax warps. Wide:
-// 4 x 128^3 multiply-adds at the 8-bit rate, 1070 cycles per tile of 128 keys,
-// beside the softmax step of eight warps.
+// Two kernels, by the query rows that share a key/value head (new rows times
+// query heads per key/value head):
+//   few, up to 16: the keys are the MMA's 128 rows and the queries its
+//     columns, hi of up to 16 rows and lo of them: S^T = K Q^T, z^T = V^T P^T
+//     with N = 32. A thread holds one key's scores of all rows, so the work
+//     follows the number of rows; a row's maximum lies across the threads, but
+//     is only needed when a weight would pass the reference, which one barrier
+//     with an OR finds out. Two groups of four warps take the groups of keys
+//     in turn, each with a summary of its own.
+//   many: 128 rows a tile, one per lane: S = Q K^T, z = P V. hi and lo of the
+//     queries go into the same accumulator (lo is not scaled there: exact down
+//     to 2^-9 of the row's largest element, off by at most 2^-17 of it below),
+//     those of the weights into two.
 //
 // Pipeline of a CTA (one per SM, persistent over its range of the list of
 // groups): warps 0, 2 and 3 fill the ring of stages, warp 1 issues the
 // products (the scores of the next group before the value product of the
-// current one), the softmax warps turn scores into weights, which go over the scores in tensor
-// memory as the value product's other operand. z stays in tensor memory; it is
-// rescaled only where a row's reference is raised or the values' scale moves.
+// current one), the softmax warps turn scores into weights. z stays in tensor
+// memory; it is rescaled only where a row's reference is raised or the values'
+// scale moves.
 //
 // Measured against the mma.sync kernel of attn_cache.cu, which this one
 // replaced for these types: its m16n8k16 products alone took 512 cycles per 32
-// keys and SM on the profiler, more than HBM's share of 370.
+// keys and SM on the profiler, more than HBM's share of 370. With few rows as
+// the 128 operand rows (a row in each of four groups of 32 lanes) an MMA of
+// 128 x 128 x 32 took 123 cycles, 1000 of the 1490 that HBM needs for a group.
 #include "attn_cache.cuh"
 
 namespace mha {
@@ -51,12 +47,9 @@ constexpr int KEYS = 128;               // keys per group
 constexpr int ROW = 128;                // bytes of a row in shared memory
 constexpr int SIDE = KEYS * ROW;        // one side of a stage
 constexpr int STAGE = 2 * SIDE;
-constexpr int STAGES = 4;
-constexpr int OPERAND = 128 * ROW;      // 128 operand rows of e4m3
-constexpr int TMEM_COLS = 512;
-constexpr int S_COL = 0;                // two score tiles of 128 columns; the weights over them
-constexpr int Z_COL = 256;              // z; wide: hi, and lo at Z_COL + 128
 constexpr float RAISE = 0.75f;          // p at most 2^0.75 (448 = 1.75 2^8)
+constexpr float NOTHING = -3e38f;       // a row's reference before its first key; finite, so that
+                                        // a masked score's distance from it is -inf too
 
 // Beside a stage: scales of its eight groups of 16 keys, which of them there
 // are, the largest vs, and whether all vs are within 2^2 of it.
@@ -66,26 +59,6 @@ struct Meta {
   float top;
   uint32_t single;
   uint32_t pad;
-};
-
-template <bool WIDE>
-struct Form {
-  static constexpr int SOFTMAX_WARPS = WIDE ? 8 : 4;
-  static constexpr int THREADS = 128 + 32 * SOFTMAX_WARPS;
-  static constexpr int ROWS = WIDE ? 128 : 16;
-  static constexpr int PIECES = WIDE ? 2 : 1;      // operand tiles of Q and of P
-  static constexpr int SUBS = WIDE ? 4 : 1;        // groups of 16 keys per lane
-  // shared memory
-  static constexpr int Q_AT = STAGES * STAGE;
-  static constexpr int M_AT = Q_AT + PIECES * OPERAND;      // narrow: four summaries' z
-  static constexpr int META_AT = M_AT + (WIDE ? 0 : 4 * 16 * 128 * 4);
-  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
-  static constexpr int LIM_AT = NAN_AT + ROWS * 16;
-  static constexpr int QF_AT = LIM_AT + ROWS * 4;
-  static constexpr int ML_AT = QF_AT + ROWS * 4;            // narrow: m, l of four summaries
-  static constexpr int FIRST_AT = ML_AT + 4 * 16 * 2 * 4;
-  static constexpr int BAR_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
-  static constexpr int SMEM = 1024 + BAR_AT + 256;
 };
 
 // D[tmem] (+)= A * B, e4m3 operands in shared memory, fp32 sums.
@@ -110,33 +83,76 @@ __device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// Instruction descriptor of kind f8f6f4: e4m3 A (K-major) and B, fp32 sums.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor of kind f8f6f4: e4m3 A and B, K-major or (1)
+// MN-major, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Half-split load of 16 columns: lane i < 16 gets columns [0, 16) of TMEM lane
-// i, lane i + 16 those at OFF of the same TMEM lane.
-template <int OFF>
-__device__ __forceinline__ void tmem_ld_x2_16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16], %17;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr), "n"(OFF));
+// Shared-memory descriptor with the 32-byte swizzle for an MN-major operand of
+// 32 columns: rows of 32 bytes, 8 of them 256 bytes.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(256 >> 4) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;  // descriptor version for tcgen05
+  d |= static_cast<uint64_t>(6) << 61;  // swizzle: 32B
+  return d;
 }
+
+// N columns of this warp's 32 TMEM lanes, one lane per thread.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else {
+    static_assert(N == 16, "columns per load");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    static_assert(N == 16, "columns per store");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  }
+}
+
 
 // Half-split stores: lane i < 16 to the columns from taddr on of TMEM lane i,
 // lane i + 16 to those at OFF of the same TMEM lane.
-template <int OFF>
-__device__ __forceinline__ void tmem_st_x2_4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2, %3, %4, %5};" ::"r"(taddr),
-               "n"(OFF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
-}
 template <int OFF>
 __device__ __forceinline__ void tmem_st_x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -147,21 +163,38 @@ __device__ __forceinline__ void tmem_st_x2_16(uint32_t taddr, const uint32_t (&r
       "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Zeros in eight columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_zero8(uint32_t taddr) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(
-                   taddr),
-               "r"(0)
-               : "memory");
-}
-
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void softmax_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Barrier that says whether any of its threads passed true.
+__device__ __forceinline__ bool named_any(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
 
 // Four values x (at most 448) as hi and lo of x = hi + lo / 2^SHIFT, four
@@ -196,57 +229,237 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // Groups of 16 keys whose values go into the next product: those of `todo`
 // within 2^2 of its largest scale `top` (and those without a positive scale,
 // so that every round takes at least one).
-__device__ __forceinline__ uint32_t take_of(const Meta* m, uint32_t todo, float& top) {
+static __device__ __noinline__ uint32_t take_of(const Meta* m, uint32_t todo, float& top) {
   top = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (todo >> i & 1) top = fmaxf(top, m->vs[i]);
   uint32_t take = 0;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if ((todo >> i & 1) && !(m->vs[i] > 0.f && m->vs[i] < 0.25f * top)) take |= 1u << i;
   return take;
 }
 
-template <bool WIDE>
-__global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
-    cache_attention_tc_kernel(const __grid_constant__ CacheAttnParams P) {
-  using F = Form<WIDE>;
-  constexpr int NST = 32 * F::SOFTMAX_WARPS;
+// Value row `row` of the stage at `src`, which not every query row sees: its
+// NaN bytes are zeroed, so that weights of 0 stay without effect, and noted for
+// the rows that do see the key at position `key`.
+static __device__ __noinline__ void mend_values(uint32_t src, int row, bool seen, int key, int rows,
+                                                const int* lim, uint32_t* nan_map) {
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t at = src + swz(row, c);
+    const uint4 u = lds128(at);
+    uint32_t x[4] = {u.x, u.y, u.z, u.w}, any = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t hit = ((x[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+      any |= hit;
+      if (hit && seen) {
+#pragma unroll 1
+        for (int byte = 0; byte < 4; ++byte) {
+          if (!(hit >> (8 * byte + 7) & 1)) continue;
+          const int d = 16 * c + 4 * w + byte;
+#pragma unroll 1
+          for (int r = 0; r < rows; ++r)
+            if (key <= lim[r]) atomicOr(nan_map + r * 4 + (d >> 5), 1u << (d & 31));
+        }
+      }
+      x[w] &= ~((hit >> 7) * 0xffu);
+    }
+    if (any) sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+  }
+}
+
+// Warp 0 fills the ring with the key tiles of groups g0 .. g0 + steps - 1, warp
+// 2 with the value tiles and the scales, each walking the groups for itself. A
+// stage is full after an arrival of each for its tiles, one for the scales, and
+// the tiles' bytes.
+template <int NS>
+__device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first, int unit,
+                                          long long g0, int steps, uint32_t stages, Meta* metas,
+                                          uint64_t* full, uint64_t* empty, const WaitCtl& ctl) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // A lane has one box of a tile: its entry j of the block table and its row in
+  // that block, moved on by 128 keys a step; warp 2's first eight lanes have 16
+  // keys' scales likewise (js, srow). Entries come from two windows of 32, the
+  // second asked for ahead of use.
+  const bool mine = lane < KEYS / P.box;
+  const int dj = KEYS / P.bt, drow = KEYS % P.bt;
+  Cursor lc = cursor_at(first, P.B, unit, g0);
+  int j, row, js, srow, kv, total, win, win_id, next_id;
+  auto table_entry = [&](int i) {
+    return i < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + i) : -1;
+  };
+  auto place = [&]() {
+    bool bad;
+    const int k0 = lc.gi * KEYS, k = k0 + (mine ? lane * P.box : 0), ks = k0 + (lane & 7) * 16;
+    total = item_of(P, lc.b, bad).total;
+    kv = lc.pr / P.tiles;
+    j = k / P.bt;
+    row = k - j * P.bt;
+    js = ks / P.bt;
+    srow = ks - js * P.bt;
+    win = __shfl_sync(0xffffffffu, j, 0);
+    win_id = table_entry(win + lane);
+    next_id = table_entry(win + 32 + lane);
+  };
+  place();
+  const CUtensorMap* map = warp == 0 ? &P.map_k : &P.map_v;
+  uint32_t tile = stages + (warp == 0 ? 0 : SIDE) + lane * P.box * ROW;
+  bool ok = true;
+  int n = 0, stage = 0;
+  uint32_t par = 1;  // a fresh barrier lets the first round pass
+  for (; n < steps; ++n) {
+    const int j0 = __shfl_sync(0xffffffffu, j, 0);
+    if (j0 + 8 >= win + 32) {  // lane i takes entry j0 + i of the two windows
+      const int at = lane + j0 - win;
+      const int x = __shfl_sync(0xffffffffu, win_id, at & 31);
+      const int y = __shfl_sync(0xffffffffu, next_id, at & 31);
+      win_id = at < 32 ? x : y;
+      win = j0;
+      next_id = table_entry(win + 32 + lane);
+    }
+    const int id = __shfl_sync(0xffffffffu, win_id, j - win);
+    const int left = total - lc.gi * KEYS;
+    const bool used = mine && lane * P.box < left;
+    const bool there = used && id >= 0 && id < P.n_blocks;
+    if (used && !there && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
+    const uint32_t load = __ballot_sync(0xffffffffu, there);
+    float ks = 0.f, vs = 0.f;
+    bool found = false;
+    if (warp == 2) {  // on their way while the stage is waited for
+      const int sid = __shfl_sync(0xffffffffu, win_id, js - win);
+      found = lane < 8 && lane * 16 < left && sid >= 0 && sid < P.n_blocks;
+      if (found) {
+        ks = __ldg(P.Ks + sid * P.h_kv + kv);
+        vs = __ldg(P.Vs + sid * P.h_kv + kv);
+      }
+    }
+    ok = __all_sync(0xffffffffu, cache_wait(empty + stage, par, ctl));
+    if (!ok) break;
+    if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(load) * P.box * ROW);
+    __syncwarp();
+    if (there) tma_load_3d_at(tile, map, full + stage, 0, row, id * P.h_kv + kv);
+    if (warp == 2) {
+      const uint32_t all = __ballot_sync(0xffffffffu, found);
+      float top = vs, least = found ? vs : 3.4e38f;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+      }
+      Meta* m = metas + stage;
+      if (lane < 8) {
+        m->ks[lane] = ks;
+        m->vs[lane] = vs;
+      }
+      if (lane == 0) {
+        m->found = all;
+        m->top = top;
+        m->single = !(least < 0.25f * top);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + stage);
+    }
+    if (++stage == NS) {
+      stage = 0;
+      par ^= 1;
+      tile -= (NS - 1) * STAGE;
+    } else {
+      tile += STAGE;
+    }
+    if (advance(lc, first, P.B, unit)) {
+      if (n + 1 < steps) place();
+    } else {
+      j += dj;
+      row += drow;
+      if (row >= P.bt) {
+        row -= P.bt;
+        ++j;
+      }
+      js += dj;
+      srow += drow;
+      if (srow >= P.bt) {
+        srow -= P.bt;
+        ++js;
+      }
+    }
+  }
+  if (!ok)  // gave up: the copies in flight are waited for before the CTA ends
+    for (int k = n > NS ? n - NS : 0; k < n; ++k) wait_in_flight(full + k % NS, (k / NS) & 1);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: S^T = K Q^T, z^T = V^T P^T
+// ---------------------------------------------------------------------------
+
+struct Few {
+  static constexpr int THREADS = 384;              // two groups of four warps for the softmax
+  static constexpr int STAGES = 6;
+  static constexpr int ROWS = 16;                  // operand rows hi at 0 .. 15, lo at 16 .. 31
+  static constexpr int TMEM_COLS = 128;
+  static constexpr int S_COL = 0;                  // per group a score tile of 32 columns
+  static constexpr int Z_COL = 64;                 // and a z of 32 columns
+  // shared memory
+  static constexpr int Q_AT = STAGES * STAGE;      // 32 operand rows
+  static constexpr int P_AT = Q_AT + 32 * ROW;     // per group a tile of 128 keys x 32
+  static constexpr int MZ_AT = P_AT;               // at a tile's end, per group 16 rows of z
+  static constexpr int META_AT = MZ_AT + 2 * ROWS * 128 * 4;
+  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
+  static constexpr int LIM_AT = NAN_AT + ROWS * 16;
+  static constexpr int QF_AT = LIM_AT + ROWS * 4;
+  static constexpr int RED_AT = QF_AT + ROWS * 4;  // per group a number per row and warp
+  static constexpr int SUM_AT = RED_AT + 2 * 4 * ROWS * 4;
+  static constexpr int MX_AT = SUM_AT + 2 * 4 * ROWS * 4;  // per group a row's reference
+  static constexpr int FIRST_AT = MX_AT + 2 * ROWS * 4;
+  static constexpr int BAR_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int SMEM = 1024 + BAR_AT + 256;
+};
+
+// NR: rows that a thread works on, at least those of a tile (1, 4, 8 or 16).
+template <int NR>
+__global__ void __launch_bounds__(Few::THREADS, 1)
+    cache_attention_few_kernel(const __grid_constant__ CacheAttnParams P) {
+  using F = Few;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta* metas = reinterpret_cast<Meta*>(smem + F::META_AT);
   int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [STAGES] tiles and scales there
-  uint64_t* empty = full + STAGES;    // [STAGES] both products done
-  uint64_t* s_full = empty + STAGES;  // [2] scores there
-  uint64_t* q_full = s_full + 2;      // the tile's queries there
-  uint64_t* p_full = q_full + 1;      // weights there
-  uint64_t* p_free = p_full + 1;      // value product done
-  uint64_t* done = p_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* empty = full + F::STAGES;    // [STAGES] both products done
+  uint64_t* s_full = empty + F::STAGES;  // [2] scores there
+  uint64_t* s_free = s_full + 2;         // [2] scores read
+  uint64_t* p_full = s_free + 2;         // [2] weights there
+  uint64_t* p_free = p_full + 2;         // [2] value product done
+  uint64_t* q_full = p_free + 2;         // the tile's queries there
+  uint64_t* done = q_full + 1;           // [2] everything of an issuing thread done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   __shared__ int warp_sums[F::THREADS / 32];
   __shared__ int abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full + s, 3);  // key tiles, value tiles, scales
-      mbar_init(empty + s, 1);
+    for (int s = 0; s < F::STAGES; ++s) {
+      mbar_init(full + s, 3);   // key tiles, value tiles, scales
+      mbar_init(empty + s, 2);  // scores and value product done
     }
-    for (int s = 0; s < 2; ++s) mbar_init(s_full + s, 1);
-    mbar_init(q_full, F::SOFTMAX_WARPS);
-    mbar_init(p_full, F::SOFTMAX_WARPS);
-    mbar_init(p_free, 1);
-    mbar_init(done, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full + s, 1);
+      mbar_init(s_free + s, 4);
+      mbar_init(p_full + s, 4);
+      mbar_init(p_free + s, 1);
+      mbar_init(done + s, 1);
+    }
+    mbar_init(q_full, 8);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.map_k);
     tma_prefetch_desc(&P.map_v);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_alloc(tmem_slot, F::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -264,102 +477,497 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
   const int steps = (int)(g1 - g0);
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
-  if (steps > 0 && warp < 4 && warp != 1) {
-    // ---- the ring: warp 0 the key tiles, warp 2 the value tiles, warp 3 the
-    // scales, each walking the groups for itself ----
-    // A lane has one box of a tile (warp 3: 16 keys of it): its entry j of the
-    // block table and its row in that block, moved on by 128 keys a step.
-    // Entries come from two windows of 32, the second asked for ahead of use.
-    const int span = warp == 3 ? 16 : P.box;
-    const bool mine = lane < KEYS / span;
-    const int dj = KEYS / P.bt, drow = KEYS % P.bt;
-    Cursor lc = cursor_at(first, P.B, unit, g0);
-    int j, row, kv, total, win, win_id, next_id;
-    auto table_entry = [&](int i) {
-      return i < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + i) : -1;
-    };
-    auto place = [&]() {
-      bool bad;
-      const int k = lc.gi * KEYS + (mine ? lane * span : 0);
-      total = item_of(P, lc.b, bad).total;
-      kv = lc.pr / P.tiles;
-      j = k / P.bt;
-      row = k - j * P.bt;
-      win = __shfl_sync(0xffffffffu, j, 0);
-      win_id = table_entry(win + lane);
-      next_id = table_entry(win + 32 + lane);
-    };
-    place();
-    const CUtensorMap* map = warp == 0 ? &P.map_k : &P.map_v;
-    const uint32_t tiles = smem_u32(smem) + (warp == 0 ? 0 : SIDE) + lane * span * ROW;
+  if (steps > 0 && (warp == 0 || warp == 2)) {
+    fill_ring<F::STAGES>(P, first, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
+  } else if (steps > 0 && warp == 1 && lane == 0) {
+    // ---- scores ----
+    // Two threads issue the products, one the scores and one the value
+    // products: a thread's instructions wait for one another, and together they
+    // took 1450 cycles a step. The columns past d_h are zeros on both sides, so
+    // all four slices of 32 are always taken.
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, 32, 0, 0);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem) + F::Q_AT, 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    Cursor cc = cursor_at(first, P.B, unit, g0);
     bool ok = true;
-    int n = 0;
-    for (; n < steps; ++n) {
-      const int stage = n % STAGES;
-      const int j0 = __shfl_sync(0xffffffffu, j, 0);
-      if (j0 + 8 >= win + 32) {  // lane i takes entry j0 + i of the two windows
-        const int at = lane + j0 - win;
-        const int x = __shfl_sync(0xffffffffu, win_id, at & 31);
-        const int y = __shfl_sync(0xffffffffu, next_id, at & 31);
-        win_id = at < 32 ? x : y;
-        win = j0;
-        next_id = table_entry(win + 32 + lane);
-      }
-      const int id = __shfl_sync(0xffffffffu, win_id, j - win);
-      const bool used = mine && lc.gi * KEYS + lane * span < total;
-      const bool there = used && id >= 0 && id < P.n_blocks;
-      const int blk = id * P.h_kv + kv;
-      if (warp == 3) {
-        // the scales are on their way while the stage is waited for
-        const float ks = there ? __ldg(P.Ks + blk) : 0.f, vs = there ? __ldg(P.Vs + blk) : 0.f;
-        const uint32_t found = __ballot_sync(0xffffffffu, there);
-        if (n >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, (n / STAGES - 1) & 1, ctl));
+    int stage = 0;
+    uint32_t par = 0, tile = 0;
+    for (int n = 0; ok && n < steps;) {
+      const int end = n + min(cc.ng - cc.gi, steps - n);  // of this tile's groups
+      ok = cache_wait(q_full, tile & 1, ctl);
+      ++tile;
+      for (; n < end; ++n) {
+        const int b = n & 1;
+        ok = ok && cache_wait(full + stage, par, ctl);
+        ok = ok && cache_wait(s_free + b, ((n >> 1) & 1) ^ 1, ctl);  // the first one passes
         if (!ok) break;
-        float top = there ? vs : 0.f, least = there ? vs : 3.4e38f;
+        tc_fence_after();
+        const uint64_t kd = k_desc + stage * (uint64_t)(STAGE >> 4);
+        const uint32_t at = tmem + F::S_COL + b * 32;
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-        }
-        Meta* m = metas + stage;
-        if (mine) {
-          m->ks[lane] = ks;
-          m->vs[lane] = vs;
-        }
-        if (lane == 0) {
-          m->found = found;
-          m->top = top;
-          m->single = !(least < 0.25f * top);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + stage);
-      } else {
-        if (used && !there && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
-        const uint32_t load = __ballot_sync(0xffffffffu, there);
-        if (n >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, (n / STAGES - 1) & 1, ctl));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(load) * span * ROW);
-        __syncwarp();
-        if (there) tma_load_3d_at(tiles + stage * STAGE, map, full + stage, 0, row, blk);
-      }
-      if (advance(lc, first, P.B, unit)) {
-        if (n + 1 < steps) place();
-      } else {
-        j += dj;
-        row += drow;
-        if (row >= P.bt) {
-          row -= P.bt;
-          ++j;
+        for (int k = 0; k < 4; ++k) umma_f8(at, kd + 2 * k, q_desc + 2 * k, idesc, k > 0);
+        umma_commit(s_full + b);
+        umma_commit(empty + stage);
+        if (++stage == F::STAGES) {
+          stage = 0;
+          par ^= 1;
         }
       }
+      cc.gi = cc.ng - 1;
+      if (n < steps) advance(cc, first, P.B, unit);
     }
-    if (!ok && warp != 3)  // gave up: the copies in flight are waited for before the CTA ends
-      for (int k = n > STAGES ? n - STAGES : 0; k < n; ++k)
-        wait_in_flight(full + k % STAGES, (k / STAGES) & 1);
+    umma_commit(done);  // what is in flight ends before tensor memory is given back
+    wait_in_flight(done, 0);
+  } else if (steps > 0 && warp == 3 && lane == 0) {
+    // ---- value products ----
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, 32, 1, 1);
+    const uint64_t p_desc = sdesc_sw32(smem_u32(smem) + F::P_AT);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem) + SIDE, 16384, 1024);
+    Cursor cc = cursor_at(first, P.B, unit, g0);
+    bool ok = true;
+    int stage = 0;
+    uint32_t par = 0;
+    uint32_t pv = 0, pv_other = 0;  // value products of this step's softmax group, of the other
+    for (int n = 0; ok && n < steps;) {
+      const int end = n + min(cc.ng - cc.gi, steps - n);
+      uint32_t held = 0;  // bit b: the z of softmax group b holds something
+      for (; n < end; ++n) {
+        const int b = n & 1;
+        ok = ok && cache_wait(full + stage, par, ctl);
+        if (!ok) break;
+        const Meta* m = metas + stage;
+        uint32_t todo = m->single ? 0u : m->found;
+        const uint64_t vd = v_desc + stage * (uint64_t)(STAGE >> 4);
+        const uint64_t pd = p_desc + b * (KEYS * 32 >> 4);
+        const uint32_t at = tmem + F::Z_COL + b * 32;
+        do {
+          if (todo) {
+            float top;
+            todo &= ~take_of(m, todo, top);
+          }
+          ok = ok && cache_wait(p_full + b, pv & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < KEYS / 32; ++k)
+            umma_f8(at, vd + k * (32 * ROW >> 4), pd + k * (32 * 32 >> 4), idesc, k > 0 || (held >> b & 1));
+          umma_commit(p_free + b);
+          held |= 1u << b;
+          ++pv;
+        } while (todo);
+        if (!ok) break;
+        umma_commit(empty + stage);
+        if (++stage == F::STAGES) {
+          stage = 0;
+          par ^= 1;
+        }
+        const uint32_t other = pv;
+        pv = pv_other;
+        pv_other = other;
+      }
+      cc.gi = cc.ng - 1;
+      if (n < steps) advance(cc, first, P.B, unit);
+    }
+    umma_commit(done + 1);
+    wait_in_flight(done + 1, 0);
+  } else if (steps > 0 && warp >= 4) {
+    // ---- softmax ----
+    // The two groups of four warps take the groups of keys in turn, each with
+    // a summary (m, l, z) of its own; thread tid has key tid of the keys and
+    // column tid of z. Once a wait has given up, the others return at once and
+    // these warps run through, so that none is missing at a barrier; what they
+    // then write means nothing, as the error word says.
+    const int grp = (warp - 4) >> 2, tid = (threadIdx.x - 128) & 127, q = warp & 3, sub = tid >> 4;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
+    const int* lim_s = reinterpret_cast<const int*>(smem + F::LIM_AT);
+    const float* qf_s = reinterpret_cast<const float*>(smem + F::QF_AT);
+    float* red = reinterpret_cast<float*>(smem + F::RED_AT) + grp * 4 * F::ROWS;  // scores' maxima
+    float* sums = reinterpret_cast<float*>(smem + F::SUM_AT);  // at a piece's end, weights' sums
+    float* refs = reinterpret_cast<float*>(smem + F::MX_AT);   // and the references
+    float* mz = reinterpret_cast<float*>(smem + F::MZ_AT);     // and z
+    const uint32_t s_at = tmem + lanes + F::S_COL + grp * 32, z_at = tmem + lanes + F::Z_COL + grp * 32;
+    // this thread's 32 bytes of the weights' tile: hi and lo, swizzled
+    const uint32_t p_at =
+        smem_u32(smem) + F::P_AT + grp * KEYS * 32 + tid * 32 + ((tid >> 2 & 1) << 4);
+    Cursor cc = cursor_at(first, P.B, unit, g0);
+    uint32_t pv = 0, s_par = 0;
+#pragma unroll 1
+    for (int n = 0; n < steps;) {
+      const int n0 = n, n1 = n + min(cc.ng - cc.gi, steps - n);  // this tile's groups
+      const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
+      // ---- the tile's queries as operand rows, and its rows' limits ----
+      bool bad;
+      const Item it = item_of(P, cc.b, bad);
+      const int all_rows = P.n_q * P.share, rows = min(F::ROWS, all_rows - rt * F::ROWS);
+      if (grp == 0) {
+        // eight threads per row, 16 elements each
+        const int r = tid >> 3, c = tid & 7;
+        const int rr = rt * F::ROWS + r, i = rr / P.share;
+        const bool in = rr < all_rows && i < it.fresh;
+        const int head = kv * P.share + (rr - i * P.share);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(P.Q) +
+            (((long long)cc.b * P.h + head) * P.n_q + i) * P.d_h + c * 16);
+        uint32_t x[8];
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (in && c * 16 < P.d_h) u = __ldg(src + e);
+          x[4 * e] = u.x;
+          x[4 * e + 1] = u.y;
+          x[4 * e + 2] = u.z;
+          x[4 * e + 3] = u.w;
+        }
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[f] << 16)),
+                                 fabsf(__uint_as_float(x[f] & 0xffff0000u))));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^(7 - E) for a largest element in [2^E, 2^(E + 1))
+        int E = (int)(__float_as_uint(top) >> 23) - 127;
+        E = E > 127 || top == 0.f ? 7 : max(E, -100);
+        const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          split4<4>(__uint_as_float(x[2 * f] << 16) * up, __uint_as_float(x[2 * f] & 0xffff0000u) * up,
+                    __uint_as_float(x[2 * f + 1] << 16) * up, __uint_as_float(x[2 * f + 1] & 0xffff0000u) * up,
+                    hi[f], lo[f]);
+        const uint32_t q_base = smem_u32(smem) + F::Q_AT;
+        sts128(q_base + swz(r, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(q_base + swz(16 + r, c), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        if (c == 0) {
+          reinterpret_cast<float*>(smem + F::QF_AT)[r] = P.cl2 * __uint_as_float((uint32_t)(E - 7 + 127) << 23);
+          reinterpret_cast<int*>(smem + F::LIM_AT)[r] =
+              !in ? -1 : P.causal_tail ? max(-1, it.total - it.fresh + i) : it.total - 1;
+        }
+      } else if (tid < F::ROWS * 4) {
+        nan_map[tid] = 0u;
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      named_sync(5, 256);
+      float qf[NR], m[NR], l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        qf[r] = qf_s[r];
+        m[r] = NOTHING;
+        l[r] = 0.f;
+      }
+      // the limits of the tile's first and last row that see a key
+      const int i0 = rt * F::ROWS / P.share;
+      const int i1 = min((rt * F::ROWS + rows - 1) / P.share, it.fresh - 1);
+      const int back = it.total - it.fresh;
+      const int lim_any = i1 < i0 ? -1 : P.causal_tail ? back + i1 : it.total - 1;
+      const int lim_all = P.causal_tail ? max(0, back + i0) : it.total - 1;
+      float vref = 1.f, per_vref = 256.f, vtop = 0.f;  // z in units of vref 2^-8; 2^8 / vref; largest vs so far
+      bool fresh = true;                               // z holds nothing yet
+
+#pragma unroll 1
+      for (n += (n ^ grp) & 1; n < n1; n += 2) {
+        const int stage = n % F::STAGES, k0 = (cc.gi + n - n0) * KEYS, key = k0 + tid;
+        cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
+        cache_wait(s_full + grp, s_par, ctl);
+        __syncwarp();
+        s_par ^= 1;
+        const Meta* meta = metas + stage;
+        float s[NR], over = -INFINITY;
+        {
+          tc_fence_after();
+          uint32_t x[NR], y[NR];
+          tmem_ld_cols<NR>(s_at, x);
+          tmem_ld_cols<NR>(s_at + 16, y);
+          const float ks = meta->ks[sub];
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + grp);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            s[r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r])) * (qf[r] * ks);
+        }
+        const uint32_t found = meta->found;
+        const bool masked = k0 + KEYS - 1 > lim_all || found != 0xffu;
+        const bool there = found >> sub & 1;
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (!there || key > lim_s[r]) s[r] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) over = fmaxf(over, s[r] - m[r]);
+        // z of this group may be changed, and its weights replaced, only behind
+        // the value products so far.
+        auto products_done = [&]() {
+          if (pv > 0) cache_wait(p_free + grp, (pv - 1) & 1, ctl);
+          __syncwarp();
+        };
+        // A row's reference is raised only where a weight would pass 2^0.75.
+        if (named_any(2 + 2 * grp, 128, over > RAISE)) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float mx = warp_max(s[r]);
+            if (lane == 0) red[r * 4 + q] = mx;
+          }
+          named_sync(1 + 2 * grp, 128);
+          uint32_t x[NR], y[NR];
+          products_done();
+          if (!fresh) {
+            tc_fence_after();
+            tmem_ld_cols<NR>(z_at, x);
+            tmem_ld_cols<NR>(z_at + 16, y);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float4 mx = *reinterpret_cast<const float4*>(red + r * 4);
+            const float top = fmaxf(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w));
+            const float to = top > m[r] + RAISE ? top : m[r];
+            const float alpha = ex2_approx(m[r] - to);
+            m[r] = to;
+            l[r] *= alpha;
+            x[r] = __float_as_uint(__uint_as_float(x[r]) * alpha);
+            y[r] = __float_as_uint(__uint_as_float(y[r]) * alpha);
+          }
+          if (!fresh) {
+            tmem_st_cols<NR>(z_at, x);
+            tmem_st_cols<NR>(z_at + 16, y);
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          s[r] = ex2_approx(s[r] - m[r]);
+          l[r] += s[r];
+        }
+        if (masked)
+          mend_values(smem_u32(smem) + stage * STAGE + SIDE, tid, there && key <= lim_any, key, F::ROWS,
+                      lim_s, nan_map);
+        // Weights, times 2^8 vs / vref with vs / vref in [2^-4, 1]. vref
+        // follows vs, a smaller one down to 2^-60 of the largest only, so
+        // that z cannot overflow. Blocks further apart go one after another.
+        uint32_t todo = meta->single ? 0u : found;
+#pragma unroll 1
+        do {
+          float top = meta->top;
+          uint32_t take = 0xffu;
+          if (todo) {
+            take = take_of(meta, todo, top);
+            todo &= ~take;
+          }
+          products_done();
+          const float seen = vtop;
+          vtop = fmaxf(vtop, top);
+          if (top > 0.f && (top > vref || top < 0.25f * vref)) {
+            const float to = fmaxf(top, vtop * 8.6736173798840355e-19f);  // 2^-60
+            if (seen > 0.f && to != vref && !fresh) {
+              const float by = vref / to;
+              uint32_t x[NR], y[NR];
+              tc_fence_after();
+              tmem_ld_cols<NR>(z_at, x);
+              tmem_ld_cols<NR>(z_at + 16, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                x[r] = __float_as_uint(__uint_as_float(x[r]) * by);
+                y[r] = __float_as_uint(__uint_as_float(y[r]) * by);
+              }
+              tmem_st_cols<NR>(z_at, x);
+              tmem_st_cols<NR>(z_at + 16, y);
+              tmem_wait_st();
+            }
+            vref = to;
+            per_vref = 256.f / to;
+          }
+          fresh = false;
+          const float f = take >> sub & 1 ? meta->vs[sub] * per_vref : 0.f;
+          uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int r = 0; r < NR; r += 4)
+            split4<4>(s[r] * f, r + 1 < NR ? s[r + 1 < NR ? r + 1 : r] * f : 0.f,
+                      r + 2 < NR ? s[r + 2 < NR ? r + 2 : r] * f : 0.f,
+                      r + 3 < NR ? s[r + 3 < NR ? r + 3 : r] * f : 0.f, hi[r / 4], lo[r / 4]);
+          sts128(p_at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(p_at ^ 16u, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          fence_async_shared();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + grp);
+          ++pv;
+        } while (todo);
+      }
+      n = n1;
+
+      // ---- the summary of the tile's keys in this range ----
+      // Both groups' parts go through shared memory (z over the weights, whose
+      // products are done, and what follows them), and the rows are merged and
+      // stored by both groups in turn.
+      if (!fresh) {
+        cache_wait(p_free + grp, (pv - 1) & 1, ctl);
+        __syncwarp();
+      }
+      named_sync(5, 256);
+      {
+        uint32_t x[NR], y[NR];
+        tc_fence_after();
+        tmem_ld_cols<NR>(z_at, x);
+        tmem_ld_cols<NR>(z_at + 16, y);
+        tmem_wait_ld();
+        tc_fence_before();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          mz[(grp * F::ROWS + r) * 128 + tid] =
+              fresh ? 0.f : fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r])) * 0.00390625f * vref;  // 2^-8
+          const float sum = warp_sum(l[r]);
+          if (lane == 0) sums[(grp * F::ROWS + r) * 4 + q] = sum;
+          if (tid == 0) refs[grp * F::ROWS + r] = m[r];
+        }
+      }
+      named_sync(5, 256);
+      const bool whole = cc.gi == 0 && n1 - n0 == cc.ng;
+      const long long slot = (2ll * blockIdx.x + (cc.gi == 0 ? 1 : 0)) * P.slot_rows;
+#pragma unroll 1
+      for (int r = grp; r < rows; r += 2) {
+        float part[2], ref[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 u = *reinterpret_cast<const float4*>(sums + (k * F::ROWS + r) * 4);
+          part[k] = u.x + u.y + u.z + u.w;
+          ref[k] = refs[k * F::ROWS + r];
+        }
+        // an empty part weighs nothing; one of NaN alone has a sum but no reference
+        const float mm = fmaxf(ref[0], ref[1]);
+        float sum = 0.f, v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (part[k] == 0.f) continue;
+          const float w = ex2_approx(ref[k] - mm);
+          sum = fmaf(w, part[k], sum);
+          v = fmaf(w, mz[(k * F::ROWS + r) * 128 + tid], v);
+        }
+        if (nan_map[r * 4 + q] >> lane & 1) v = __int_as_float(0x7fffffff);
+        const bool none = lim_s[r] < 0 || sum == 0.f;
+        if (whole) {
+          const int rr = rt * F::ROWS + r, i = rr / P.share, head = kv * P.share + (rr - i * P.share);
+          if (tid < P.d_vh)
+            static_cast<__nv_bfloat16*>(P.Z)[((long long)cc.b * P.n_q + i) * P.h * P.d_vh +
+                                             (long long)head * P.d_vh + tid] =
+                __float2bfloat16_rn(none ? 0.f : v / sum);
+        } else {
+          float* const pz = P.part + 4ll * P.ranges * P.slot_rows;
+          if (tid < P.d_vh) pz[(slot + r) * P.d_vh + tid] = none ? 0.f : v;
+          if (tid == 0) {
+            P.part[2 * (slot + r)] = none ? -INFINITY : mm;
+            P.part[2 * (slot + r) + 1] = none ? 0.f : sum;
+          }
+        }
+      }
+      named_sync(5, 256);  // read, before the next tile's limits are written
+      cc.gi = cc.ng - 1;
+      if (n < steps) advance(cc, first, P.B, unit);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, F::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: S = Q K^T, z = P V
+// ---------------------------------------------------------------------------
+
+struct Many {
+  static constexpr int SOFTMAX_WARPS = 8;
+  static constexpr int THREADS = 128 + 32 * SOFTMAX_WARPS;
+  static constexpr int STAGES = 4;
+  static constexpr int ROWS = 128;
+  static constexpr int PIECES = 2;                 // hi and lo of Q and of P
+  static constexpr int SUBS = 4;                   // groups of 16 keys per lane
+  static constexpr int OPERAND = 128 * ROW;        // 128 operand rows of e4m3
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int S_COL = 0;                  // two score tiles of 128 columns; the weights over them
+  static constexpr int Z_COL = 256;                // hi's z, and lo's at Z_COL + 128
+  // shared memory
+  static constexpr int Q_AT = STAGES * STAGE;
+  static constexpr int META_AT = Q_AT + PIECES * OPERAND;
+  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
+  static constexpr int LIM_AT = NAN_AT + ROWS * 16;
+  static constexpr int QF_AT = LIM_AT + ROWS * 4;
+  static constexpr int FIRST_AT = QF_AT + ROWS * 4;
+  static constexpr int BAR_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int SMEM = 1024 + BAR_AT + 256;
+};
+
+__global__ void __launch_bounds__(Many::THREADS, 1)
+    cache_attention_many_kernel(const __grid_constant__ CacheAttnParams P) {
+  using F = Many;
+  constexpr int NST = 32 * F::SOFTMAX_WARPS;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Meta* metas = reinterpret_cast<Meta*>(smem + F::META_AT);
+  int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [F::STAGES] tiles and scales there
+  uint64_t* empty = full + F::STAGES;    // [F::STAGES] both products done
+  uint64_t* s_full = empty + F::STAGES;  // [2] scores there
+  uint64_t* q_full = s_full + 2;      // the tile's queries there
+  uint64_t* p_full = q_full + 1;      // [2] weights there
+  uint64_t* p_free = p_full + 2;      // value product done
+  uint64_t* done = p_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  __shared__ int warp_sums[F::THREADS / 32];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F::STAGES; ++s) {
+      mbar_init(full + s, 3);  // key tiles, value tiles, scales
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full + s, 1);
+      mbar_init(p_full + s, F::SOFTMAX_WARPS);
+    }
+    mbar_init(q_full, F::SOFTMAX_WARPS);
+    mbar_init(p_free, 1);
+    mbar_init(done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&P.map_k);
+    tma_prefetch_desc(&P.map_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, F::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  scan_groups<F::THREADS, KEYS>(P, first, warp_sums);
+
+  const int unit = P.h_kv * P.tiles;
+  const long long G = (long long)first[P.B] * unit;
+  const long long g0 = blockIdx.x * G / P.ranges, g1 = (blockIdx.x + 1) * G / P.ranges;
+  const int steps = (int)(g1 - g0);
+  const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
+
+  if (steps > 0 && (warp == 0 || warp == 2)) {
+    fill_ring<F::STAGES>(P, first, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- products ----
-    constexpr uint32_t idesc_s = idesc_e4m3_f32(128, KEYS, 0);
-    const uint32_t idesc_z = idesc_e4m3_f32(128, P.d_vh, 1);
+    constexpr uint32_t idesc_s = idesc_e4m3_f32(128, KEYS, 0, 0);
+    const uint32_t idesc_z = idesc_e4m3_f32(128, P.d_vh, 0, 1);
     const int slices = (P.d_h + 31) / 32;
     const uint32_t base = smem_u32(smem);
     const uint64_t q_desc = sdesc_sw128(base + F::Q_AT, 16, 1024);
@@ -367,28 +975,29 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
     const uint64_t v_desc = sdesc_sw128(base + SIDE, 16384, 1024);
     Cursor cc = cursor_at(first, P.B, unit, g0);
     bool ok = true, begins = true;
-    int tile = 0, pv = 0;
+    int tile = 0;
+    uint32_t pv = 0, pv_other = 0;  // value products of groups like this one (even or odd), of the others
     auto issue_s = [&](int n) {
-      const int stage = n % STAGES, b = n & 1;
+      const int stage = n % F::STAGES, b = n & 1;
       // The scores go over the weights of group n - 2, whose value product is
       // ahead of them in this thread's order.
-      ok = ok && mbar_wait(full + stage, (n / STAGES) & 1, ctl);
+      ok = ok && cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
       if (!ok) return;
       tc_fence_after();
       const uint64_t kd = k_desc + (uint64_t)(stage * STAGE >> 4);
 #pragma unroll
       for (int p = 0; p < F::PIECES; ++p) {
         for (int k = 0; k < slices; ++k)
-          umma_f8(tmem + S_COL + b * KEYS, q_desc + (uint64_t)((p * OPERAND + k * 32) >> 4),
+          umma_f8(tmem + F::S_COL + b * KEYS, q_desc + (uint64_t)((p * F::OPERAND + k * 32) >> 4),
                   kd + (uint64_t)(k * 32 >> 4), idesc_s, p + k > 0);
       }
       umma_commit(s_full + b);
     };
     for (int n = 0; ok && n < steps; ++n) {
-      const int stage = n % STAGES;
+      const int stage = n % F::STAGES;
       const bool ends = cc.gi == cc.ng - 1 || n == steps - 1;
       if (begins) {
-        ok = mbar_wait(q_full, tile & 1, ctl);
+        ok = cache_wait(q_full, tile & 1, ctl);
         ++tile;
         issue_s(n);
       }
@@ -402,7 +1011,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
           float top;
           todo &= ~take_of(m, todo, top);
         }
-        if (!mbar_wait(p_full, pv & 1, ctl)) {
+        if (!cache_wait(p_full + (n & 1), pv & 1, ctl)) {
           ok = false;
           break;
         }
@@ -412,7 +1021,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
         for (int p = 0; p < F::PIECES; ++p) {
 #pragma unroll
           for (int k = 0; k < KEYS / 32; ++k)
-            umma_f8_ts(tmem + Z_COL + p * 128, tmem + S_COL + (n & 1) * KEYS + p * 32 + k * 8,
+            umma_f8_ts(tmem + F::Z_COL + p * 128, tmem + F::S_COL + (n & 1) * KEYS + p * 32 + k * 8,
                        vd + (uint64_t)(k * 32 * ROW >> 4), idesc_z, !fresh || k > 0);
         }
         umma_commit(p_free);
@@ -421,6 +1030,9 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
       } while (todo);
       if (!ok) break;
       umma_commit(empty + stage);
+      const uint32_t other = pv;
+      pv = pv_other;
+      pv_other = other;
       begins = ends;
       advance(cc, first, P.B, unit);
     }
@@ -428,19 +1040,18 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
     wait_in_flight(done, 0);
   } else if (steps > 0 && warp >= 4) {
     // ---- softmax ----
-    // Lane i < 16 of a warp holds the first half of row i's keys, lane i + 16
-    // the other: 16 keys each of the warp's 32 (narrow) or 64 each (wide).
+    // A warp has 16 rows: lane i < 16 holds the first 64 keys of row i, lane
+    // i + 16 the others.
     const int q = warp & 3, hh = (warp - 4) >> 2, half = lane >> 4;
     const int tid = threadIdx.x - 128;
-    const int row = WIDE ? 32 * q + 16 * hh + (lane & 15) : lane & 15;
-    const uint32_t lanes = static_cast<uint32_t>(WIDE ? 32 * q + 16 * hh : 32 * q) << 16;
-    const uint32_t lo_lanes = 16u << 16;  // narrow: from a row's hi to its lo
+    const int row = 32 * q + 16 * hh + (lane & 15);
+    const uint32_t lanes = static_cast<uint32_t>(32 * q + 16 * hh) << 16;
     uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
     int* lim_s = reinterpret_cast<int*>(smem + F::LIM_AT);
     float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
     const uint32_t q_base = smem_u32(smem) + F::Q_AT;
     Cursor cc = cursor_at(first, P.B, unit, g0);
-    bool ok = true, begins = true;
+    bool begins = true;
     int pv = 0, start_gi = 0;
     int limit = -1, lim_all = 0, lim_any = -1;
     float qf = 0.f, m = -INFINITY, l = 0.f, vref = 1.f, vtop = 0.f;
@@ -452,7 +1063,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
       const Item it = item_of(P, cc.b, bad);
       const int rows = P.n_q * P.share;
       {
-        constexpr int TPR = WIDE ? 2 : 8;     // threads per row
+        constexpr int TPR = 2;     // threads per row
         constexpr int PPT = 8 / TPR;          // 16-element pieces per thread
         const int r = tid / TPR, part = tid % TPR;
         const int rr = rt * F::ROWS + r, i = rr / P.share;
@@ -489,23 +1100,15 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
           for (int f = 0; f < 4; ++f) {
             const uint4 u = raw[k][f / 2];
             const uint32_t x0 = f % 2 ? u.z : u.x, x1 = f % 2 ? u.w : u.y;
-            split4<WIDE ? 0 : 4>(__uint_as_float(x0 << 16) * up, __uint_as_float(x0 & 0xffff0000u) * up,
+            split4<0>(__uint_as_float(x0 << 16) * up, __uint_as_float(x0 & 0xffff0000u) * up,
                                  __uint_as_float(x1 << 16) * up, __uint_as_float(x1 & 0xffff0000u) * up,
                                  hi[f], lo[f]);
           }
           const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           const int c = part * PPT + k;
-          if constexpr (WIDE) {
-            sts128(q_base + swz(r, c), h4);
-            sts128(q_base + OPERAND + swz(r, c), l4);
-          } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              sts128(q_base + swz(32 * w + r, c), h4);
-              sts128(q_base + swz(32 * w + 16 + r, c), l4);
-            }
-          }
+          sts128(q_base + swz(r, c), h4);
+          sts128(q_base + F::OPERAND + swz(r, c), l4);
         }
         if (part == 0) {
           qf_s[r] = P.cl2 * __uint_as_float((uint32_t)(E - 7 + 127) << 23);
@@ -515,9 +1118,9 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      softmax_sync<NST>();
+      named_sync(1, NST);
       for (int e = tid; e < F::ROWS * 4; e += NST) nan_map[e] = 0u;  // the last tile's was read
-      softmax_sync<NST>();
+      named_sync(1, NST);
       qf = qf_s[row];
       limit = lim_s[row];
       // the limits of the tile's first and last row that see a key
@@ -538,7 +1141,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
       tc_fence_after();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const uint32_t at = tmem + lanes + Z_COL + (WIDE ? p * 128u : p * lo_lanes);
+        const uint32_t at = tmem + lanes + F::Z_COL + p * 128u;
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
           uint32_t o[32];
@@ -552,14 +1155,15 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
       tmem_wait_st();
     };
 
+#pragma unroll 1
     for (int n = 0; n < steps; ++n) {
-      const int stage = n % STAGES, b = n & 1;
+      const int stage = n % F::STAGES, b = n & 1;
       const bool ends = cc.gi == cc.ng - 1 || n == steps - 1;
       if (begins) begin_tile();
-      ok = ok && mbar_wait(full + stage, (n / STAGES) & 1, ctl);
-      ok = ok && mbar_wait(s_full + b, (n >> 1) & 1, ctl);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
+      cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
+      cache_wait(s_full + b, (n >> 1) & 1, ctl);
+      __syncwarp();
+      {
         tc_fence_after();
         const Meta* meta = metas + stage;
         const int kb = cc.gi * KEYS;
@@ -567,24 +1171,14 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
         const bool masked = kb + KEYS - 1 > lim_all || found != 0xffu;
         float s[F::SUBS][16];
         {
-          const uint32_t at = tmem + lanes + S_COL + b * KEYS;
-          if constexpr (WIDE) {
-            uint32_t x[64];
-            tmem_ld_x2_64<64>(at, x);
-            tmem_wait_ld();
+          const uint32_t at = tmem + lanes + F::S_COL + b * KEYS;
+          uint32_t x[64];
+          tmem_ld_x2_64<64>(at, x);
+          tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 64; ++k) s[k / 16][k % 16] = __uint_as_float(x[k]);
-          } else {
-            uint32_t x[16], y[16];
-            tmem_ld_x2_16<16>(at + 32 * q, x);
-            tmem_ld_x2_16<16>(at + 32 * q + lo_lanes, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              s[0][k] = fmaf(__uint_as_float(y[k]), 0.0625f, __uint_as_float(x[k]));
-          }
+          for (int k = 0; k < 64; ++k) s[k / 16][k % 16] = __uint_as_float(x[k]);
         }
-        const int sub0 = WIDE ? 4 * half : 2 * q + half;  // this lane's groups of 16 keys
+        const int sub0 = 4 * half;  // this lane's groups of 16 keys
         float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < F::SUBS; ++i) {
@@ -614,40 +1208,17 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
             l += s[i][k];
           }
         }
-        if (masked && tid < KEYS) {
-          // Value rows that not every row sees, or none: their NaN bytes are
-          // zeroed, and noted for the rows that do see them.
-          const uint32_t src = smem_u32(smem) + stage * STAGE + SIDE;
-          const bool there = found >> (tid >> 4) & 1;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            const uint32_t at = src + swz(tid, c);
-            const uint4 u = lds128(at);
-            uint32_t x[4] = {u.x, u.y, u.z, u.w}, any = 0;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t hit = ((x[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              any |= hit;
-              if (hit && there && kb + tid <= lim_any) {
-                for (int byte = 0; byte < 4; ++byte) {
-                  if (!(hit >> (8 * byte + 7) & 1)) continue;
-                  const int d = 16 * c + 4 * w + byte;
-                  for (int r = 0; r < F::ROWS; ++r)
-                    if (kb + tid <= lim_s[r]) atomicOr(nan_map + r * 4 + (d >> 5), 1u << (d & 31));
-                }
-              }
-              x[w] &= ~((hit >> 7) * 0xffu);
-            }
-            if (any) sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
-          }
-        }
+        if (masked && tid < KEYS)
+          mend_values(smem_u32(smem) + stage * STAGE + SIDE, tid,
+                      (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, F::ROWS, lim_s, nan_map);
         // Weights, times 2^8 vs / vref with vs / vref in [2^-4, 1]. vref
         // follows vs, a smaller one down to 2^-60 of the largest only, so
         // that z cannot overflow. Blocks further apart go one after another.
         uint32_t todo = meta->single ? 0u : found;
         bool fresh = begins;  // z holds nothing yet
         bool again = false;   // a further round
-        const uint32_t p_at = tmem + lanes + S_COL + b * KEYS;
+        const uint32_t p_at = tmem + lanes + F::S_COL + b * KEYS;
+#pragma unroll 1
         do {
           float top = meta->top;
           uint32_t take = found;
@@ -669,8 +1240,8 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
           const float f = alpha * by;
           const bool scales = !fresh && __any_sync(0xffffffffu, f != 1.f);
           if (scales || again) {
-            ok = __all_sync(0xffffffffu, mbar_wait(p_free, (pv - 1) & 1, ctl));
-            if (!ok) break;
+            cache_wait(p_free, (pv - 1) & 1, ctl);
+            __syncwarp();
             if (scales) scale_z(f);
           }
           alpha = 1.f;
@@ -685,28 +1256,22 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
               split4<4>(s[i][4 * k] * r, s[i][4 * k + 1] * r, s[i][4 * k + 2] * r, s[i][4 * k + 3] * r,
                         hi[4 * i + k], lo[4 * i + k]);
           }
-          if constexpr (WIDE) {
-            tmem_st_x2_16<16>(p_at, hi);
-            tmem_st_x2_16<16>(p_at + 32, lo);
-          } else {
-            tmem_st_x2_4<4>(p_at + 8 * q, hi);
-            tmem_st_x2_4<4>(p_at + 8 * q + lo_lanes, lo);
-            // no weight for the other warps' keys
-            tmem_zero8(p_at + ((8 * q + 8) & 31));
-            tmem_zero8(p_at + ((8 * q + 16) & 31));
-            tmem_zero8(p_at + ((8 * q + 24) & 31));
-          }
+          tmem_st_x2_16<16>(p_at, hi);
+          tmem_st_x2_16<16>(p_at + 32, lo);
           tmem_wait_st();
           if (masked) fence_async_shared();  // value rows may have been mended
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full);
+          if (lane == 0) mbar_arrive(p_full + b);  // a warp may be a group ahead of another
           ++pv;
         } while (todo);
       }
       if (ends) {
         // ---- the summary of the keys [start_gi, cc.gi] of the tile ----
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(p_free, (pv - 1) & 1, ctl));
+        // (one phase after the other: the parity tells two apart, not three)
+        if (pv > 1) cache_wait(p_free, (pv - 2) & 1, ctl);
+        cache_wait(p_free, (pv - 1) & 1, ctl);
+        __syncwarp();
         tc_fence_after();
         const bool whole = start_gi == 0 && cc.gi == cc.ng - 1;
         const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
@@ -738,90 +1303,24 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
               z[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         };
-        if constexpr (WIDE) {
-          const float scale = none ? 0.f : 0.00390625f * (whole ? 1.f / l : 1.f);  // 2^-8
-          if (ok && !whole && half == 0 && rt * F::ROWS + row < P.n_q * P.share) {
-            P.part[2 * (slot * P.slot_rows + row)] = none ? -INFINITY : m;
-            P.part[2 * (slot * P.slot_rows + row) + 1] = none ? 0.f : l;
-          }
+        const float scale = none ? 0.f : 0.00390625f * (whole ? 1.f / l : 1.f);  // 2^-8
+        if (!whole && half == 0 && rt * F::ROWS + row < P.n_q * P.share) {
+          P.part[2 * (slot * P.slot_rows + row)] = none ? -INFINITY : m;
+          P.part[2 * (slot * P.slot_rows + row) + 1] = none ? 0.f : l;
+        }
 #pragma unroll
-          for (int cb = 0; cb < 2; ++cb) {
-            if (!ok) continue;
-            uint32_t x[32], y[32];
-            tmem_ld_x2_32<64>(tmem + lanes + Z_COL + 32 * cb, x);
-            tmem_ld_x2_32<64>(tmem + lanes + Z_COL + 128 + 32 * cb, y);
-            tmem_wait_ld();
+        for (int cb = 0; cb < 2; ++cb) {
+          uint32_t x[32], y[32];
+          tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + 32 * cb, x);
+          tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + 128 + 32 * cb, y);
+          tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; c += 16) {
-              float v[16];
+          for (int c = 0; c < 32; c += 16) {
+            float v[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                v[k] = none ? 0.f : fmaf(__uint_as_float(y[c + k]), 0.0625f, __uint_as_float(x[c + k])) * vref;
-              store(row, 64 * half + 32 * cb + c, v, scale);
-            }
-          }
-        } else {
-          // four warps' summaries of the same rows, merged in shared memory
-          float* mz = reinterpret_cast<float*>(smem + F::M_AT);   // [4][16][128], pieces of 4 swizzled
-          float* ml = reinterpret_cast<float*>(smem + F::ML_AT);  // [4][16][2]
-          if (half == 0) {
-            ml[(q * 16 + row) * 2] = none ? -INFINITY : m;
-            ml[(q * 16 + row) * 2 + 1] = none ? 0.f : l;
-          }
-#pragma unroll
-          for (int cb = 0; cb < 2; ++cb) {
-            if (!ok) continue;
-            uint32_t x[32], y[32];
-            tmem_ld_x2_32<64>(tmem + lanes + Z_COL + 32 * cb, x);
-            tmem_ld_x2_32<64>(tmem + lanes + lo_lanes + Z_COL + 32 * cb, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              float v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = none ? 0.f
-                            : fmaf(__uint_as_float(y[c + k]), 0.0625f, __uint_as_float(x[c + k])) * 0.00390625f * vref;
-              const int piece = (64 * half + 32 * cb + c) >> 2;
-              *reinterpret_cast<float4*>(mz + (q * 16 + row) * 128 + ((piece ^ (row & 7)) << 2)) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-            }
-          }
-          softmax_sync<NST>();
-          const int r = tid >> 3, c = (tid & 7) * 16;
-          float mm = -INFINITY, ll = 0.f, w4[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[(w * 16 + r) * 2]);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float mw = ml[(w * 16 + r) * 2], lw = ml[(w * 16 + r) * 2 + 1];
-            // the empty summary weighs nothing; a NaN one has no m but an l
-            w4[w] = mw == mm ? 1.f : ex2_approx(mw - mm);
-            if (mw == -INFINITY && lw == 0.f) w4[w] = 0.f;
-            ll += w4[w] * lw;
-          }
-          float v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if (w4[w] == 0.f) continue;
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 u = *reinterpret_cast<const float4*>(mz + (w * 16 + r) * 128 +
-                                                               ((((c + k) >> 2) ^ (r & 7)) << 2));
-              v[k] = fmaf(w4[w], u.x, v[k]);
-              v[k + 1] = fmaf(w4[w], u.y, v[k + 1]);
-              v[k + 2] = fmaf(w4[w], u.z, v[k + 2]);
-              v[k + 3] = fmaf(w4[w], u.w, v[k + 3]);
-            }
-          }
-          if (ok) {
-            if (!whole && (tid & 7) == 0 && rt * F::ROWS + r < P.n_q * P.share) {
-              P.part[2 * (slot * P.slot_rows + r)] = mm;
-              P.part[2 * (slot * P.slot_rows + r) + 1] = ll;
-            }
-            store(r, c, v, whole ? (ll == 0.f ? 0.f : 1.f / ll) : 1.f);
+            for (int k = 0; k < 16; ++k)
+              v[k] = none ? 0.f : fmaf(__uint_as_float(y[c + k]), 0.0625f, __uint_as_float(x[c + k])) * vref;
+            store(row, 64 * half + 32 * cb + c, v, scale);
           }
         }
         tc_fence_before();
@@ -834,16 +1333,14 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, F::TMEM_COLS);
   }
 }
 
-template <bool WIDE>
-cudaError_t launch(const CacheAttnParams& P, int ctas, cudaStream_t s) {
-  auto* kernel = cache_attention_tc_kernel<WIDE>;
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), Form<WIDE>::SMEM))
-    return cudaErrorUnknown;
-  return launch_dependent(kernel, dim3(ctas), dim3(Form<WIDE>::THREADS), Form<WIDE>::SMEM, s, P);
+template <typename K>
+cudaError_t launch(K* kernel, int threads, int smem, const CacheAttnParams& P, cudaStream_t s) {
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorUnknown;
+  return launch_dependent(kernel, dim3(P.ranges), dim3(threads), smem, s, P);
 }
 
 }  // namespace
@@ -852,9 +1349,18 @@ mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s) {
   int box = KEYS;  // the largest box that blocks are made of
   while (P.bt % box) box /= 2;
   if (!make_cache_maps(P, box, ROW)) return MHA_ERR_CUDA;
-  const int ctas = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
-  P.ranges = ctas;
-  cudaError_t e = P.tile_rows == 16 ? launch<false>(P, ctas, s) : launch<true>(P, ctas, s);
+  P.ranges = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
+  cudaError_t e;
+  if (P.tile_rows == Many::ROWS)
+    e = launch(cache_attention_many_kernel, Many::THREADS, Many::SMEM, P, s);
+  else if (P.slot_rows == 1)
+    e = launch(cache_attention_few_kernel<1>, Few::THREADS, Few::SMEM, P, s);
+  else if (P.slot_rows <= 4)
+    e = launch(cache_attention_few_kernel<4>, Few::THREADS, Few::SMEM, P, s);
+  else if (P.slot_rows <= 8)
+    e = launch(cache_attention_few_kernel<8>, Few::THREADS, Few::SMEM, P, s);
+  else
+    e = launch(cache_attention_few_kernel<16>, Few::THREADS, Few::SMEM, P, s);
   if (e == cudaSuccess) e = launch_cache_merge(P, MHA_DTYPE_BF16, s);
   count_launch(2);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
