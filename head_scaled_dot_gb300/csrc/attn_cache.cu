@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  scan_groups<CA_THREADS, S::SK>(P, first, warp_sums);
+  scan_groups<CA_THREADS, S::SK>(P, first, nullptr, warp_sums);
   const int unit = P.h_kv * P.tiles;
   const long long G = (long long)first[P.B] * unit;
   const int w = blockIdx.x * CA_WARPS + warp;
@@ -693,14 +693,15 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
     if (w0 == w1) return;
     const float* ml = P.part;
     const float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows;
+#pragma unroll 2
     for (int w = w0 + pg; w <= w1; w += PG) {
       const long long s0 = w * G / P.ranges;
-      if (s0 == (w + 1) * G / P.ranges) continue;  // a warp without work
+      if (s0 == (w + 1) * G / P.ranges) continue;  // a range without work
       const long long at = (2ll * w + (s0 <= a ? 1 : 0)) * P.slot_rows + row;
       const float mw = ml[2 * at], lw = ml[2 * at + 1];
-      if (mw == -INFINITY && lw == 0.f) continue;  // the empty summary
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (col < P.d_vh) v = *reinterpret_cast<const float4*>(pz + at * P.d_vh + col);
+      if (mw == -INFINITY && lw == 0.f) continue;  // the empty summary
       const float mn = fmaxf(m, mw);
       const float x = m == mn ? 1.f : exp2f(m - mn), y = mw == mn ? 1.f : exp2f(mw - mn);
       acc.x = acc.x * x + v.x * y;

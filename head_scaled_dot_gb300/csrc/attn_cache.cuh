@@ -61,10 +61,12 @@ __device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& b
 }
 
 // first[b], b = 0 .. B: groups of SK keys per tile of rows before batch item
-// b. Every CTA computes them; the first one leaves them in the workspace and
-// reports lengths out of bounds. All threads of the CTA.
+// b; totals[b] (unless null): its keys. Every CTA computes them; the first one
+// leaves them in the workspace and reports lengths out of bounds. All threads
+// of the CTA.
 template <int THREADS, int SK>
-__device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first, int* warp_sums) {
+__device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first, int* totals,
+                                            int* warp_sums) {
   constexpr int PER = (MHA_MAX_PADDED_BATCH + THREADS - 1) / THREADS;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int n[PER], sum = 0;
@@ -77,6 +79,7 @@ __device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first
       const Item it = item_of(P, b, bad);
       if (bad && blockIdx.x == 0 && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
       if (it.fresh > 0) n[k] = (it.total + SK - 1) / SK;
+      if (totals) totals[b] = it.total;
     }
     sum += n[k];
   }
@@ -170,6 +173,11 @@ static __device__ __noinline__ void wait_in_flight(uint64_t* bar, uint32_t parit
     if (globaltimer_ns() - t0 > 100000000ull) return;
   }
 }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;

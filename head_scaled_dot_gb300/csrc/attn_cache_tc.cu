@@ -9,7 +9,7 @@
 //   queries  a row is scaled by a power of two to a largest element in
 //            [2^7, 2^8). bf16's 8 bits are exactly the 4 of hi and the 4 of
 //            lo, down to 2^-13 of the row's largest element.
-//   weights  p = 2^{s - m}, times 2^8 vs / vref: 8 bits, down to 2^-18 of the
+//   weights  p = 2^{s - m}, times 2^7 vs / vref: 8 bits, down to 2^-17 of the
 //            weight of the row's reference m.
 //
 // Two kernels, by the query rows that share a key/value head (new rows times
@@ -47,7 +47,9 @@ constexpr int KEYS = 128;               // keys per group
 constexpr int ROW = 128;                // bytes of a row in shared memory
 constexpr int SIDE = KEYS * ROW;        // one side of a stage
 constexpr int STAGE = 2 * SIDE;
-constexpr float RAISE = 0.75f;          // p at most 2^0.75 (448 = 1.75 2^8)
+constexpr float RAISE = 1.75f;          // a weight is at most 2^1.75 ...
+constexpr float UNIT = 128.f;           // ... times this: e4m3's largest is 448 > 2^8.75
+constexpr float HEADROOM = 1.f;         // few rows: references are set above the scores seen
 constexpr float NOTHING = -3e38f;       // a row's reference before its first key; finite, so that
                                         // a masked score's distance from it is -inf too
 
@@ -177,12 +179,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // Barrier that says whether any of its threads passed true.
 __device__ __forceinline__ bool named_any(int id, int threads, bool v) {
   uint32_t r;
@@ -276,9 +272,9 @@ static __device__ __noinline__ void mend_values(uint32_t src, int row, bool seen
 // stage is full after an arrival of each for its tiles, one for the scales, and
 // the tiles' bytes.
 template <int NS>
-__device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first, int unit,
-                                          long long g0, int steps, uint32_t stages, Meta* metas,
-                                          uint64_t* full, uint64_t* empty, const WaitCtl& ctl) {
+__device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first,
+                                          const int* totals, int unit, long long g0, int steps,
+                                          uint32_t stages, Meta* metas, uint64_t* full, uint64_t* empty, const WaitCtl& ctl) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // A lane has one box of a tile: its entry j of the block table and its row in
   // that block, moved on by 128 keys a step; warp 2's first eight lanes have 16
@@ -292,9 +288,8 @@ __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* f
     return i < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + i) : -1;
   };
   auto place = [&]() {
-    bool bad;
     const int k0 = lc.gi * KEYS, k = k0 + (mine ? lane * P.box : 0), ks = k0 + (lane & 7) * 16;
-    total = item_of(P, lc.b, bad).total;
+    total = totals[lc.b];
     kv = lc.pr / P.tiles;
     j = k / P.bt;
     row = k - j * P.bt;
@@ -406,15 +401,19 @@ struct Few {
   static constexpr int P_AT = Q_AT + 32 * ROW;     // per group a tile of 128 keys x 32
   static constexpr int MZ_AT = P_AT;               // at a tile's end, per group 16 rows of z
   static constexpr int META_AT = MZ_AT + 2 * ROWS * 128 * 4;
-  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
-  static constexpr int LIM_AT = NAN_AT + ROWS * 16;
-  static constexpr int QF_AT = LIM_AT + ROWS * 4;
-  static constexpr int RED_AT = QF_AT + ROWS * 4;  // per group a number per row and warp
+  static constexpr int RAW_AT = MZ_AT + ROWS * 128 * 4;     // until then: the next tile's queries as they are
+  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);  // what follows twice, for this tile and the next
+  static constexpr int LIM_AT = NAN_AT + 2 * ROWS * 16;
+  static constexpr int QF_AT = LIM_AT + 2 * ROWS * 4;
+  static constexpr int RED_AT = QF_AT + 2 * ROWS * 4;       // per group a number per row and warp
   static constexpr int SUM_AT = RED_AT + 2 * 4 * ROWS * 4;
-  static constexpr int MX_AT = SUM_AT + 2 * 4 * ROWS * 4;  // per group a row's reference
-  static constexpr int FIRST_AT = MX_AT + 2 * ROWS * 4;
-  static constexpr int BAR_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int MX_AT = SUM_AT + 2 * 8 * ROWS * 4;   // per group a row's reference
+  static constexpr int WGT_AT = MX_AT + 2 * ROWS * 4;       // and its weight in the merge
+  static constexpr int FIRST_AT = WGT_AT + 2 * ROWS * 4;
+  static constexpr int TOTAL_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int BAR_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
   static constexpr int SMEM = 1024 + BAR_AT + 256;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 // NR: rows that a thread works on, at least those of a tile (1, 4, 8 or 16).
@@ -427,6 +426,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta* metas = reinterpret_cast<Meta*>(smem + F::META_AT);
   int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
+  int* totals = reinterpret_cast<int*>(smem + F::TOTAL_AT);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [STAGES] tiles and scales there
   uint64_t* empty = full + F::STAGES;    // [STAGES] both products done
   uint64_t* s_full = empty + F::STAGES;  // [2] scores there
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
       mbar_init(p_free + s, 1);
       mbar_init(done + s, 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, 4);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.map_k);
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 
   grid_dep_wait();
   grid_dep_launch_dependents();
-  scan_groups<F::THREADS, KEYS>(P, first, warp_sums);
+  scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
 
   const int unit = P.h_kv * P.tiles;
   const long long G = (long long)first[P.B] * unit;
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
+    fill_ring<F::STAGES>(P, first, totals, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- scores ----
     // Two threads issue the products, one the scores and one the value
@@ -579,93 +579,112 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     // then write means nothing, as the error word says.
     const int grp = (warp - 4) >> 2, tid = (threadIdx.x - 128) & 127, q = warp & 3, sub = tid >> 4;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
-    const int* lim_s = reinterpret_cast<const int*>(smem + F::LIM_AT);
-    const float* qf_s = reinterpret_cast<const float*>(smem + F::QF_AT);
     float* red = reinterpret_cast<float*>(smem + F::RED_AT) + grp * 4 * F::ROWS;  // scores' maxima
-    float* sums = reinterpret_cast<float*>(smem + F::SUM_AT);  // at a piece's end, weights' sums
-    float* refs = reinterpret_cast<float*>(smem + F::MX_AT);   // and the references
+    float* sums = reinterpret_cast<float*>(smem + F::SUM_AT);  // at a piece's end, weights' sums,
+    float* refs = reinterpret_cast<float*>(smem + F::MX_AT);   // the references,
+    float2* wgt = reinterpret_cast<float2*>(smem + F::WGT_AT); // both groups' weights in the merge
     float* mz = reinterpret_cast<float*>(smem + F::MZ_AT);     // and z
     const uint32_t s_at = tmem + lanes + F::S_COL + grp * 32, z_at = tmem + lanes + F::Z_COL + grp * 32;
     // this thread's 32 bytes of the weights' tile: hi and lo, swizzled
     const uint32_t p_at =
         smem_u32(smem) + F::P_AT + grp * KEYS * 32 + tid * 32 + ((tid >> 2 & 1) << 4);
+    const int rows = P.n_q * P.share;  // at most 16: a tile is a key/value head
     Cursor cc = cursor_at(first, P.B, unit, g0);
-    uint32_t pv = 0, s_par = 0;
-#pragma unroll 1
-    for (int n = 0; n < steps;) {
-      const int n0 = n, n1 = n + min(cc.ng - cc.gi, steps - n);  // this tile's groups
-      const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
-      // ---- the tile's queries as operand rows, and its rows' limits ----
-      bool bad;
-      const Item it = item_of(P, cc.b, bad);
-      const int all_rows = P.n_q * P.share, rows = min(F::ROWS, all_rows - rt * F::ROWS);
-      if (grp == 0) {
-        // eight threads per row, 16 elements each
-        const int r = tid >> 3, c = tid & 7;
-        const int rr = rt * F::ROWS + r, i = rr / P.share;
-        const bool in = rr < all_rows && i < it.fresh;
-        const int head = kv * P.share + (rr - i * P.share);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(P.Q) +
-            (((long long)cc.b * P.h + head) * P.n_q + i) * P.d_h + c * 16);
-        uint32_t x[8];
-        float top = 0.f;
+
+    // A tile's queries, by group 1: eight threads per row, 16 elements each.
+    // They are copied to shared memory a tile ahead (fetch_q), and made operand
+    // rows as soon as the last scores of the tile before are there (make_q).
+    const int qr = tid >> 3, qc = tid & 7, qi = qr / P.share;
+    const bool q_mine = qr < rows && qc * 16 < P.d_h;
+    auto fetch_q = [&](const Cursor& c) {
+      if (!q_mine) return;
+      const int head = c.pr * P.share + (qr - qi * P.share);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(P.Q) +
+                                 (((long long)c.b * P.h + head) * P.n_q + qi) * P.d_h + qc * 16;
+      cp_async16(smem_u32(smem) + F::RAW_AT + tid * 32, src);
+      cp_async16(smem_u32(smem) + F::RAW_AT + tid * 32 + 16, src + 8);
+    };
+    auto make_q = [&](const Item& it, int par) {
+      cp_async_wait_all();
+      const bool in = qr < rows && qi < it.fresh;
+      uint32_t x[8];
+      float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (in && c * 16 < P.d_h) u = __ldg(src + e);
-          x[4 * e] = u.x;
-          x[4 * e + 1] = u.y;
-          x[4 * e + 2] = u.z;
-          x[4 * e + 3] = u.w;
-        }
+      for (int e = 0; e < 2; ++e) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (in && q_mine) u = lds128(smem_u32(smem) + F::RAW_AT + tid * 32 + 16 * e);
+        x[4 * e] = u.x;
+        x[4 * e + 1] = u.y;
+        x[4 * e + 2] = u.z;
+        x[4 * e + 3] = u.w;
+      }
 #pragma unroll
-        for (int f = 0; f < 8; ++f)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[f] << 16)),
-                                 fabsf(__uint_as_float(x[f] & 0xffff0000u))));
+      for (int k = 0; k < 8; ++k)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)),
+                               fabsf(__uint_as_float(x[k] & 0xffff0000u))));
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^(7 - E) for a largest element in [2^E, 2^(E + 1))
-        int E = (int)(__float_as_uint(top) >> 23) - 127;
-        E = E > 127 || top == 0.f ? 7 : max(E, -100);
-        const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
-        uint32_t hi[4], lo[4];
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // 2^(7 - E) for a largest element in [2^E, 2^(E + 1))
+      int E = (int)(__float_as_uint(top) >> 23) - 127;
+      E = E > 127 || top == 0.f ? 7 : max(E, -100);
+      const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+      uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          split4<4>(__uint_as_float(x[2 * f] << 16) * up, __uint_as_float(x[2 * f] & 0xffff0000u) * up,
-                    __uint_as_float(x[2 * f + 1] << 16) * up, __uint_as_float(x[2 * f + 1] & 0xffff0000u) * up,
-                    hi[f], lo[f]);
-        const uint32_t q_base = smem_u32(smem) + F::Q_AT;
-        sts128(q_base + swz(r, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(q_base + swz(16 + r, c), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        if (c == 0) {
-          reinterpret_cast<float*>(smem + F::QF_AT)[r] = P.cl2 * __uint_as_float((uint32_t)(E - 7 + 127) << 23);
-          reinterpret_cast<int*>(smem + F::LIM_AT)[r] =
-              !in ? -1 : P.causal_tail ? max(-1, it.total - it.fresh + i) : it.total - 1;
-        }
-      } else if (tid < F::ROWS * 4) {
-        nan_map[tid] = 0u;
+      for (int k = 0; k < 4; ++k)
+        split4<4>(__uint_as_float(x[2 * k] << 16) * up, __uint_as_float(x[2 * k] & 0xffff0000u) * up,
+                  __uint_as_float(x[2 * k + 1] << 16) * up, __uint_as_float(x[2 * k + 1] & 0xffff0000u) * up,
+                  hi[k], lo[k]);
+      const uint32_t q_base = smem_u32(smem) + F::Q_AT;
+      sts128(q_base + swz(qr, qc), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sts128(q_base + swz(16 + qr, qc), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if (qc == 0) {
+        reinterpret_cast<float*>(smem + F::QF_AT)[par * F::ROWS + qr] =
+            P.cl2 * __uint_as_float((uint32_t)(E - 7 + 127) << 23);
+        reinterpret_cast<int*>(smem + F::LIM_AT)[par * F::ROWS + qr] =
+            !in ? -1 : P.causal_tail ? max(-1, it.total - it.fresh + qi) : it.total - 1;
       }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      named_sync(5, 256);
+    };
+
+    bool bad;
+    Item it = item_of(P, cc.b, bad);
+    if (grp == 1) {
+      fetch_q(cc);
+      make_q(it, 0);
+    } else if (tid < F::ROWS * 4) {
+      reinterpret_cast<uint32_t*>(smem + F::NAN_AT)[tid] = 0u;
+    }
+    uint32_t pv = 0, s_par = 0;
+    int tpar = 0;
+#pragma unroll 1
+    for (int n = 0; n < steps; tpar ^= 1) {
+      const int n0 = n, n1 = n + min(cc.ng - cc.gi, steps - n);  // this tile's groups
+      uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT) + tpar * F::ROWS * 4;
+      const int* lim_s = reinterpret_cast<const int*>(smem + F::LIM_AT) + tpar * F::ROWS;
+      named_sync(5, 256);  // the tile's limits are there; everything of the tile before is read
+      // the next tile: its item and its queries are on their way from here on
+      Cursor nc = cc;
+      nc.gi = nc.ng - 1;
+      if (n1 < steps) advance(nc, first, P.B, unit);
+      const Item next = item_of(P, nc.b < P.B ? nc.b : cc.b, bad);
+      if (grp == 1 && n1 < steps) fetch_q(nc);
+      if (grp == 0 && tid < F::ROWS * 4)
+        reinterpret_cast<uint32_t*>(smem + F::NAN_AT)[(tpar ^ 1) * F::ROWS * 4 + tid] = 0u;
       float qf[NR], m[NR], l[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        qf[r] = qf_s[r];
+        qf[r] = reinterpret_cast<const float*>(smem + F::QF_AT)[tpar * F::ROWS + r];
         m[r] = NOTHING;
         l[r] = 0.f;
       }
       // the limits of the tile's first and last row that see a key
-      const int i0 = rt * F::ROWS / P.share;
-      const int i1 = min((rt * F::ROWS + rows - 1) / P.share, it.fresh - 1);
-      const int back = it.total - it.fresh;
-      const int lim_any = i1 < i0 ? -1 : P.causal_tail ? back + i1 : it.total - 1;
-      const int lim_all = P.causal_tail ? max(0, back + i0) : it.total - 1;
-      float vref = 1.f, per_vref = 256.f, vtop = 0.f;  // z in units of vref 2^-8; 2^8 / vref; largest vs so far
-      bool fresh = true;                               // z holds nothing yet
+      const int i1 = min((rows - 1) / P.share, it.fresh - 1), back = it.total - it.fresh;
+      const int lim_any = i1 < 0 ? -1 : P.causal_tail ? back + i1 : it.total - 1;
+      const int lim_all = P.causal_tail ? max(0, back) : it.total - 1;
+      float vref = 1.f, per_vref = UNIT, vtop = 0.f;  // z in units of vref / UNIT; largest vs so far
+      bool fresh = true;                              // z holds nothing yet
 
 #pragma unroll 1
       for (n += (n ^ grp) & 1; n < n1; n += 2) {
@@ -706,7 +725,10 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
           if (pv > 0) cache_wait(p_free + grp, (pv - 1) & 1, ctl);
           __syncwarp();
         };
-        // A row's reference is raised only where a weight would pass 2^0.75.
+        // References are raised only where a weight would pass 2^1.75, then those
+        // of all rows, to twice the largest weight so far: the further passes
+        // through this part, which 16 rows would otherwise take every few
+        // steps, cost more than the bit.
         if (named_any(2 + 2 * grp, 128, over > RAISE)) {
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
@@ -726,7 +748,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
           for (int r = 0; r < NR; ++r) {
             const float4 mx = *reinterpret_cast<const float4*>(red + r * 4);
             const float top = fmaxf(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w));
-            const float to = top > m[r] + RAISE ? top : m[r];
+            const float to = fmaxf(m[r], top + HEADROOM);
             const float alpha = ex2_approx(m[r] - to);
             m[r] = to;
             l[r] *= alpha;
@@ -747,7 +769,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         if (masked)
           mend_values(smem_u32(smem) + stage * STAGE + SIDE, tid, there && key <= lim_any, key, F::ROWS,
                       lim_s, nan_map);
-        // Weights, times 2^8 vs / vref with vs / vref in [2^-4, 1]. vref
+        // Weights, times 2^7 vs / vref with vs / vref in [2^-4, 1]. vref
         // follows vs, a smaller one down to 2^-60 of the largest only, so
         // that z cannot overflow. Blocks further apart go one after another.
         uint32_t todo = meta->single ? 0u : found;
@@ -781,7 +803,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
               tmem_wait_st();
             }
             vref = to;
-            per_vref = 256.f / to;
+            per_vref = UNIT / to;
           }
           fresh = false;
           const float f = take >> sub & 1 ? meta->vs[sub] * per_vref : 0.f;
@@ -811,64 +833,81 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         __syncwarp();
       }
       named_sync(5, 256);
+      if (grp == 1 && n1 < steps) {
+        make_q(next, tpar ^ 1);
+        named_sync(3, 128);  // z goes over the queries
+      }
       {
+        float* mine = mz + grp * F::ROWS * 128;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          mine[r * 128 + tid] = l[r];
+          if (tid == 0) refs[grp * F::ROWS + r] = m[r];
+        }
+        named_sync(1 + 2 * grp, 128);
+        if (qr < rows) {  // eight threads per row
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 u = *reinterpret_cast<const float4*>(mine + qr * 128 + k * 32 + qc * 4);
+            sum += u.x + u.y + (u.z + u.w);
+          }
+          sums[(grp * F::ROWS + qr) * 8 + qc] = sum;
+        }
+        named_sync(1 + 2 * grp, 128);
         uint32_t x[NR], y[NR];
         tc_fence_after();
         tmem_ld_cols<NR>(z_at, x);
         tmem_ld_cols<NR>(z_at + 16, y);
         tmem_wait_ld();
         tc_fence_before();
+        const float unit_v = vref / UNIT;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          mz[(grp * F::ROWS + r) * 128 + tid] =
-              fresh ? 0.f : fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r])) * 0.00390625f * vref;  // 2^-8
-          const float sum = warp_sum(l[r]);
-          if (lane == 0) sums[(grp * F::ROWS + r) * 4 + q] = sum;
-          if (tid == 0) refs[grp * F::ROWS + r] = m[r];
-        }
+        for (int r = 0; r < NR; ++r)
+          mine[r * 128 + tid] = fresh ? 0.f : fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r])) * unit_v;
       }
       named_sync(5, 256);
       const bool whole = cc.gi == 0 && n1 - n0 == cc.ng;
       const long long slot = (2ll * blockIdx.x + (cc.gi == 0 ? 1 : 0)) * P.slot_rows;
-#pragma unroll 1
-      for (int r = grp; r < rows; r += 2) {
-        float part[2], ref[2];
+      if (grp == 0 && tid < rows) {  // a row's two parts: weights, sum and reference
+        const int r = tid;
+        float part[2], w[2] = {0.f, 0.f}, sum = 0.f;
+        const float mm = fmaxf(refs[r], refs[F::ROWS + r]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float4 u = *reinterpret_cast<const float4*>(sums + (k * F::ROWS + r) * 4);
-          part[k] = u.x + u.y + u.z + u.w;
-          ref[k] = refs[k * F::ROWS + r];
-        }
-        // an empty part weighs nothing; one of NaN alone has a sum but no reference
-        const float mm = fmaxf(ref[0], ref[1]);
-        float sum = 0.f, v = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
+          const float4* u = reinterpret_cast<const float4*>(sums + (k * F::ROWS + r) * 8);
+          part[k] = u[0].x + u[0].y + (u[0].z + u[0].w) + (u[1].x + u[1].y + (u[1].z + u[1].w));
+          // an empty part weighs nothing; one of NaN alone has a sum but no reference
           if (part[k] == 0.f) continue;
-          const float w = ex2_approx(ref[k] - mm);
-          sum = fmaf(w, part[k], sum);
-          v = fmaf(w, mz[(k * F::ROWS + r) * 128 + tid], v);
+          w[k] = ex2_approx(refs[k * F::ROWS + r] - mm);
+          sum = fmaf(w[k], part[k], sum);
         }
-        if (nan_map[r * 4 + q] >> lane & 1) v = __int_as_float(0x7fffffff);
         const bool none = lim_s[r] < 0 || sum == 0.f;
-        if (whole) {
-          const int rr = rt * F::ROWS + r, i = rr / P.share, head = kv * P.share + (rr - i * P.share);
-          if (tid < P.d_vh)
-            static_cast<__nv_bfloat16*>(P.Z)[((long long)cc.b * P.n_q + i) * P.h * P.d_vh +
-                                             (long long)head * P.d_vh + tid] =
-                __float2bfloat16_rn(none ? 0.f : v / sum);
-        } else {
-          float* const pz = P.part + 4ll * P.ranges * P.slot_rows;
-          if (tid < P.d_vh) pz[(slot + r) * P.d_vh + tid] = none ? 0.f : v;
-          if (tid == 0) {
-            P.part[2 * (slot + r)] = none ? -INFINITY : mm;
-            P.part[2 * (slot + r) + 1] = none ? 0.f : sum;
-          }
+        const float per = none ? 0.f : whole ? 1.f / sum : 1.f;
+        wgt[r] = none ? make_float2(0.f, 0.f) : make_float2(w[0] * per, w[1] * per);
+        if (!whole) {
+          P.part[2 * (slot + r)] = none ? -INFINITY : mm;
+          P.part[2 * (slot + r) + 1] = none ? 0.f : sum;
         }
       }
-      named_sync(5, 256);  // read, before the next tile's limits are written
-      cc.gi = cc.ng - 1;
-      if (n < steps) advance(cc, first, P.B, unit);
+      named_sync(5, 256);
+#pragma unroll 4
+      for (int r = grp; r < rows; r += 2) {
+        const float2 w = wgt[r];
+        float v = fmaf(w.x, mz[r * 128 + tid], w.y * mz[(F::ROWS + r) * 128 + tid]);
+        if (nan_map[r * 4 + q] >> lane & 1) v = __int_as_float(0x7fffffff);
+        if (w.x == 0.f && w.y == 0.f) v = 0.f;
+        if (tid >= P.d_vh) continue;
+        if (whole) {
+          const int i = r / P.share, head = cc.pr * P.share + (r - i * P.share);
+          static_cast<__nv_bfloat16*>(P.Z)[(((long long)cc.b * P.n_q + i) * P.h + head) * P.d_vh + tid] =
+              __float2bfloat16_rn(v);
+        } else {
+          P.part[4ll * P.ranges * P.slot_rows + (slot + r) * P.d_vh + tid] = v;
+        }
+      }
+      cc = nc;
+      it = next;
     }
   }
   tc_fence_before();
@@ -901,7 +940,8 @@ struct Many {
   static constexpr int LIM_AT = NAN_AT + ROWS * 16;
   static constexpr int QF_AT = LIM_AT + ROWS * 4;
   static constexpr int FIRST_AT = QF_AT + ROWS * 4;
-  static constexpr int BAR_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int TOTAL_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
+  static constexpr int BAR_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
   static constexpr int SMEM = 1024 + BAR_AT + 256;
 };
 
@@ -914,6 +954,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta* metas = reinterpret_cast<Meta*>(smem + F::META_AT);
   int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
+  int* totals = reinterpret_cast<int*>(smem + F::TOTAL_AT);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [F::STAGES] tiles and scales there
   uint64_t* empty = full + F::STAGES;    // [F::STAGES] both products done
   uint64_t* s_full = empty + F::STAGES;  // [2] scores there
@@ -954,7 +995,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
 
   grid_dep_wait();
   grid_dep_launch_dependents();
-  scan_groups<F::THREADS, KEYS>(P, first, warp_sums);
+  scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
 
   const int unit = P.h_kv * P.tiles;
   const long long G = (long long)first[P.B] * unit;
@@ -963,7 +1004,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
+    fill_ring<F::STAGES>(P, first, totals, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- products ----
     constexpr uint32_t idesc_s = idesc_e4m3_f32(128, KEYS, 0, 0);
@@ -1192,7 +1233,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        // a row's reference is raised only where a weight would pass 2^0.75
+        // a row's reference is raised only where a weight would pass 2^1.75
         float alpha = 1.f;
         if (mx > m + RAISE) {
           alpha = ex2_approx(m - mx);
@@ -1211,7 +1252,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         if (masked && tid < KEYS)
           mend_values(smem_u32(smem) + stage * STAGE + SIDE, tid,
                       (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, F::ROWS, lim_s, nan_map);
-        // Weights, times 2^8 vs / vref with vs / vref in [2^-4, 1]. vref
+        // Weights, times 2^7 vs / vref with vs / vref in [2^-4, 1]. vref
         // follows vs, a smaller one down to 2^-60 of the largest only, so
         // that z cannot overflow. Blocks further apart go one after another.
         uint32_t todo = meta->single ? 0u : found;
@@ -1250,7 +1291,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           uint32_t hi[4 * F::SUBS], lo[4 * F::SUBS];
 #pragma unroll
           for (int i = 0; i < F::SUBS; ++i) {
-            const float r = take >> (sub0 + i) & 1 ? 256.f * (meta->vs[sub0 + i] / vref) : 0.f;
+            const float r = take >> (sub0 + i) & 1 ? UNIT * (meta->vs[sub0 + i] / vref) : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               split4<4>(s[i][4 * k] * r, s[i][4 * k + 1] * r, s[i][4 * k + 2] * r, s[i][4 * k + 3] * r,
@@ -1303,7 +1344,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
               z[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         };
-        const float scale = none ? 0.f : 0.00390625f * (whole ? 1.f / l : 1.f);  // 2^-8
+        const float scale = none ? 0.f : (1.f / UNIT) * (whole ? 1.f / l : 1.f);
         if (!whole && half == 0 && rt * F::ROWS + row < P.n_q * P.share) {
           P.part[2 * (slot * P.slot_rows + row)] = none ? -INFINITY : m;
           P.part[2 * (slot * P.slot_rows + row) + 1] = none ? 0.f : l;
