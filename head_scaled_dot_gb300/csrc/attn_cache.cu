@@ -16,9 +16,9 @@
 // the cache is streamed once and memory is the bound.
 //
 // Work split. The 8-bit rows of every (batch item, key/value head, tile of 16
-// rows) form one list of groups of SK keys; warp w of all W warps takes the
-// equal contiguous range [w G / W, (w + 1) G / W) whatever the lengths, which
-// the kernel reads on the device. A range that covers a tile's keys whole
+// rows) form one list of groups of SK keys; each warp takes a contiguous range
+// of it, of equal cost whatever the lengths, which the kernel reads on the
+// device. A range that covers a tile's keys whole
 // writes z / l; otherwise each piece's summary goes to the workspace and
 // cache_merge_kernel merges a tile's pieces in order. No warp waits for
 // another one.
@@ -163,16 +163,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   grid_dep_launch_dependents();
 
   scan_groups<CA_THREADS, S::SK>(P, first, nullptr, warp_sums);
-  const int unit = P.h_kv * P.tiles;
-  const long long G = (long long)first[P.B] * unit;
-  const int w = blockIdx.x * CA_WARPS + warp;
-  const long long g0 = w * G / P.ranges;
-  const long long g1 = (w + 1) * G / P.ranges;
-  if (g0 >= g1) return;
+  const Ranges ranges(P, first[P.B]);
+  const int unit = ranges.unit, w = blockIdx.x * CA_WARPS + warp;
+  Cursor cc, past;  // what is computed; the next range's first
+  const int g0 = ranges.begin(w, first, P.B, cc);
+  int left = ranges.begin(w + 1, first, P.B, past) - g0, load_left = left;
+  if (left <= 0) return;
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
-
-  Cursor cc = cursor_at(first, P.B, unit, g0);  // what is computed
-  int left = (int)(g1 - g0), load_left = left;
   const uint32_t ring = smem_u32(smem) + warp * S::N * S::BYTES;
   const uint32_t metas = smem_u32(smem) + S::RING + warp * S::N * S::SUBS * 16;
 
@@ -678,9 +675,7 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
   const int i = (int)(bi % P.n_q), b = (int)(bi / P.n_q);
   const int kv = head / P.share, r = i * P.share + head % P.share;
   const int pr = kv * P.tiles + r / P.tile_rows, row = r % P.tile_rows;
-  const int unit = P.h_kv * P.tiles;
-  const int f0 = P.first[b], ng = P.first[b + 1] - f0;
-  const long long G = (long long)P.first[P.B] * unit;
+  const int ng = P.first[b + 1] - P.first[b];
   const int col = threadIdx.x % CT * 4, pg = threadIdx.x / CT;
   T* out = static_cast<T*>(P.Z) + (bi * P.h + head) * P.d_vh + col;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -688,16 +683,22 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
   bool bad;
   const Item it = item_of(P, b, bad);
   if (ng > 0) {
-    const long long a = (long long)f0 * unit + (long long)pr * ng;
-    const int w0 = (int)(((a + 1) * P.ranges - 1) / G), w1 = (int)(((a + ng) * P.ranges - 1) / G);
+    const Ranges ranges(P, P.first[P.B]);
+    const int w0 = ranges.owner(P.first, b, pr, 0, ng), w1 = ranges.owner(P.first, b, pr, ng - 1, ng);
     if (w0 == w1) return;
+    // Of the tile's ranges the first has it from its first group on (slot 2 w
+    // + 1); the others come upon it in the middle (slot 2 w), but for those
+    // that have no group at all, as when there are more ranges than groups.
+    const int cost = (P.first[b] + ranges.cost * b) * ranges.unit + pr * (ng + ranges.cost) + ranges.cost;
     const float* ml = P.part;
     const float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows;
 #pragma unroll 2
     for (int w = w0 + pg; w <= w1; w += PG) {
-      const long long s0 = w * G / P.ranges;
-      if (s0 == (w + 1) * G / P.ranges) continue;  // a range without work
-      const long long at = (2ll * w + (s0 <= a ? 1 : 0)) * P.slot_rows + row;
+      // its units [u, v) of the costs, as the tile's groups
+      const int u = w * ranges.per + min(w, ranges.more) - cost;
+      const int v1 = u + ranges.per + (w < ranges.more ? 1 : 0);
+      if (max(v1, 0) <= max(u, 0)) continue;
+      const long long at = (2ll * w + (u <= 0 ? 1 : 0)) * P.slot_rows + row;
       const float mw = ml[2 * at], lw = ml[2 * at + 1];
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (col < P.d_vh) v = *reinterpret_cast<const float4*>(pz + at * P.d_vh + col);
@@ -751,6 +752,7 @@ mha_status launch(CacheAttnParams& P, cudaStream_t s) {
   if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), Stage<D>::SMEM)) return MHA_ERR_CUDA;
   const int ctas = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
   P.ranges = ctas * CA_WARPS;
+  P.tile_cost = 1;
   cudaError_t e = launch_dependent(kernel, dim3(ctas), dim3(CA_THREADS), Stage<D>::SMEM, s, P);
   if (e == cudaSuccess) e = launch_cache_merge(P, F32 ? MHA_DTYPE_F32 : MHA_DTYPE_BF16, s);
   count_launch(2);

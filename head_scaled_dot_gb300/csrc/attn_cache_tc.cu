@@ -267,13 +267,12 @@ static __device__ __noinline__ void mend_values(uint32_t src, int row, bool seen
   }
 }
 
-// Warp 0 fills the ring with the key tiles of groups g0 .. g0 + steps - 1, warp
-// 2 with the value tiles and the scales, each walking the groups for itself. A
+// Warp 0 fills the ring with the key tiles of the groups from lc on, warp 2 with the value tiles and the scales, each walking the groups for itself. A
 // stage is full after an arrival of each for its tiles, one for the scales, and
 // the tiles' bytes.
 template <int NS>
 __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first,
-                                          const int* totals, int unit, long long g0, int steps,
+                                          const int* totals, int unit, Cursor lc, int steps,
                                           uint32_t stages, Meta* metas, uint64_t* full, uint64_t* empty, const WaitCtl& ctl) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // A lane has one box of a tile: its entry j of the block table and its row in
@@ -282,7 +281,6 @@ __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* f
   // second asked for ahead of use.
   const bool mine = lane < KEYS / P.box;
   const int dj = KEYS / P.bt, drow = KEYS % P.bt;
-  Cursor lc = cursor_at(first, P.B, unit, g0);
   int j, row, js, srow, kv, total, win, win_id, next_id;
   auto table_entry = [&](int i) {
     return i < P.max_blocks ? __ldg(P.table + (long long)lc.b * P.max_blocks + i) : -1;
@@ -408,8 +406,8 @@ struct Few {
   static constexpr int RED_AT = QF_AT + 2 * ROWS * 4;       // per group a number per row and warp
   static constexpr int SUM_AT = RED_AT + 2 * 4 * ROWS * 4;
   static constexpr int MX_AT = SUM_AT + 2 * 8 * ROWS * 4;   // per group a row's reference
-  static constexpr int WGT_AT = MX_AT + 2 * ROWS * 4;       // and its weight in the merge
-  static constexpr int FIRST_AT = WGT_AT + 2 * ROWS * 4;
+  static constexpr int WGT_AT = MX_AT + 2 * ROWS * 4;       // and what the merge needs of it
+  static constexpr int FIRST_AT = WGT_AT + 4 * ROWS * 4;
   static constexpr int TOTAL_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
   static constexpr int BAR_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
   static constexpr int SMEM = 1024 + BAR_AT + 256;
@@ -438,6 +436,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   __shared__ int warp_sums[F::THREADS / 32];
   __shared__ int abort_flag;
+  __shared__ Cursor start;
+  __shared__ int bounds[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -471,14 +471,20 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
   grid_dep_launch_dependents();
   scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
 
-  const int unit = P.h_kv * P.tiles;
-  const long long G = (long long)first[P.B] * unit;
-  const long long g0 = blockIdx.x * G / P.ranges, g1 = (blockIdx.x + 1) * G / P.ranges;
-  const int steps = (int)(g1 - g0);
+  // this CTA's range: where it begins, and its groups (found by one thread of
+  // two warps)
+  if ((threadIdx.x & ~32u) == 0) {
+    const int k = threadIdx.x >> 5;
+    Cursor c;
+    bounds[k] = Ranges(P, first[P.B]).begin(blockIdx.x + k, first, P.B, c);
+    if (k == 0) start = c;
+  }
+  __syncthreads();
+  const int unit = P.h_kv * P.tiles, steps = bounds[1] - bounds[0];
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, totals, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
+    fill_ring<F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- scores ----
     // Two threads issue the products, one the scores and one the value
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     constexpr uint32_t idesc = idesc_e4m3_f32(128, 32, 0, 0);
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem) + F::Q_AT, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
-    Cursor cc = cursor_at(first, P.B, unit, g0);
+    Cursor cc = start;
     bool ok = true;
     int stage = 0;
     uint32_t par = 0, tile = 0;
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     constexpr uint32_t idesc = idesc_e4m3_f32(128, 32, 1, 1);
     const uint64_t p_desc = sdesc_sw32(smem_u32(smem) + F::P_AT);
     const uint64_t v_desc = sdesc_sw128(smem_u32(smem) + SIDE, 16384, 1024);
-    Cursor cc = cursor_at(first, P.B, unit, g0);
+    Cursor cc = start;
     bool ok = true;
     int stage = 0;
     uint32_t par = 0;
@@ -582,14 +588,14 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     float* red = reinterpret_cast<float*>(smem + F::RED_AT) + grp * 4 * F::ROWS;  // scores' maxima
     float* sums = reinterpret_cast<float*>(smem + F::SUM_AT);  // at a piece's end, weights' sums,
     float* refs = reinterpret_cast<float*>(smem + F::MX_AT);   // the references,
-    float2* wgt = reinterpret_cast<float2*>(smem + F::WGT_AT); // both groups' weights in the merge
+    float4* wgt = reinterpret_cast<float4*>(smem + F::WGT_AT); // a row's two weights, its place, whether NaN is due
     float* mz = reinterpret_cast<float*>(smem + F::MZ_AT);     // and z
     const uint32_t s_at = tmem + lanes + F::S_COL + grp * 32, z_at = tmem + lanes + F::Z_COL + grp * 32;
     // this thread's 32 bytes of the weights' tile: hi and lo, swizzled
     const uint32_t p_at =
         smem_u32(smem) + F::P_AT + grp * KEYS * 32 + tid * 32 + ((tid >> 2 & 1) << 4);
     const int rows = P.n_q * P.share;  // at most 16: a tile is a key/value head
-    Cursor cc = cursor_at(first, P.B, unit, g0);
+    Cursor cc = start;
 
     // A tile's queries, by group 1: eight threads per row, 16 elements each.
     // They are copied to shared memory a tile ahead (fetch_q), and made operand
@@ -884,26 +890,29 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         }
         const bool none = lim_s[r] < 0 || sum == 0.f;
         const float per = none ? 0.f : whole ? 1.f / sum : 1.f;
-        wgt[r] = none ? make_float2(0.f, 0.f) : make_float2(w[0] * per, w[1] * per);
+        const int i = r / P.share, head = cc.pr * P.share + (r - i * P.share);
+        const uint4 nans = *reinterpret_cast<const uint4*>(nan_map + r * 4);
+        wgt[r] = make_float4(none ? 0.f : w[0] * per, none ? 0.f : w[1] * per,
+                             __int_as_float(whole ? (cc.b * P.n_q + i) * P.h + head : (int)slot + r),
+                             __int_as_float(nans.x | nans.y | nans.z | nans.w));
         if (!whole) {
           P.part[2 * (slot + r)] = none ? -INFINITY : mm;
           P.part[2 * (slot + r) + 1] = none ? 0.f : sum;
         }
       }
       named_sync(5, 256);
-#pragma unroll 4
-      for (int r = grp; r < rows; r += 2) {
-        const float2 w = wgt[r];
-        float v = fmaf(w.x, mz[r * 128 + tid], w.y * mz[(F::ROWS + r) * 128 + tid]);
-        if (nan_map[r * 4 + q] >> lane & 1) v = __int_as_float(0x7fffffff);
-        if (w.x == 0.f && w.y == 0.f) v = 0.f;
-        if (tid >= P.d_vh) continue;
-        if (whole) {
-          const int i = r / P.share, head = cc.pr * P.share + (r - i * P.share);
-          static_cast<__nv_bfloat16*>(P.Z)[(((long long)cc.b * P.n_q + i) * P.h + head) * P.d_vh + tid] =
-              __float2bfloat16_rn(v);
-        } else {
-          P.part[4ll * P.ranges * P.slot_rows + (slot + r) * P.d_vh + tid] = v;
+      if (tid < P.d_vh) {
+#pragma unroll 2
+        for (int r = grp; r < rows; r += 2) {
+          const float4 w = wgt[r];
+          float v = fmaf(w.x, mz[r * 128 + tid], w.y * mz[(F::ROWS + r) * 128 + tid]);
+          if (__float_as_int(w.w) != 0 && (nan_map[r * 4 + q] >> lane & 1)) v = __int_as_float(0x7fffffff);
+          if (w.x == 0.f && w.y == 0.f) v = 0.f;
+          const long long at = (long long)__float_as_int(w.z) * P.d_vh + tid;
+          if (whole)
+            static_cast<__nv_bfloat16*>(P.Z)[at] = __float2bfloat16_rn(v);
+          else
+            P.part[4ll * P.ranges * P.slot_rows + at] = v;
         }
       }
       cc = nc;
@@ -965,6 +974,8 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ int warp_sums[F::THREADS / 32];
   __shared__ int abort_flag;
+  __shared__ Cursor start;
+  __shared__ int bounds[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -997,14 +1008,20 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   grid_dep_launch_dependents();
   scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
 
-  const int unit = P.h_kv * P.tiles;
-  const long long G = (long long)first[P.B] * unit;
-  const long long g0 = blockIdx.x * G / P.ranges, g1 = (blockIdx.x + 1) * G / P.ranges;
-  const int steps = (int)(g1 - g0);
+  // this CTA's range: where it begins, and its groups (found by one thread of
+  // two warps)
+  if ((threadIdx.x & ~32u) == 0) {
+    const int k = threadIdx.x >> 5;
+    Cursor c;
+    bounds[k] = Ranges(P, first[P.B]).begin(blockIdx.x + k, first, P.B, c);
+    if (k == 0) start = c;
+  }
+  __syncthreads();
+  const int unit = P.h_kv * P.tiles, steps = bounds[1] - bounds[0];
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, totals, unit, g0, steps, smem_u32(smem), metas, full, empty, ctl);
+    fill_ring<F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- products ----
     constexpr uint32_t idesc_s = idesc_e4m3_f32(128, KEYS, 0, 0);
@@ -1014,7 +1031,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
     const uint64_t q_desc = sdesc_sw128(base + F::Q_AT, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(base, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(base + SIDE, 16384, 1024);
-    Cursor cc = cursor_at(first, P.B, unit, g0);
+    Cursor cc = start;
     bool ok = true, begins = true;
     int tile = 0;
     uint32_t pv = 0, pv_other = 0;  // value products of groups like this one (even or odd), of the others
@@ -1091,7 +1108,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
     int* lim_s = reinterpret_cast<int*>(smem + F::LIM_AT);
     float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
     const uint32_t q_base = smem_u32(smem) + F::Q_AT;
-    Cursor cc = cursor_at(first, P.B, unit, g0);
+    Cursor cc = start;
     bool begins = true;
     int pv = 0, start_gi = 0;
     int limit = -1, lim_all = 0, lim_any = -1;
@@ -1391,6 +1408,7 @@ mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s) {
   while (P.bt % box) box /= 2;
   if (!make_cache_maps(P, box, ROW)) return MHA_ERR_CUDA;
   P.ranges = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
+  P.tile_cost = P.tile_rows == Many::ROWS ? 3 : 2 + P.slot_rows / 4;
   cudaError_t e;
   if (P.tile_rows == Many::ROWS)
     e = launch(cache_attention_many_kernel, Many::THREADS, Many::SMEM, P, s);
