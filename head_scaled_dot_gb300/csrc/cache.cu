@@ -117,31 +117,45 @@ __global__ void __launch_bounds__(RES_THREADS) reserve_kernel(const __grid_const
     if (threadIdx.x == 0) *P.n_free_out = n_free - s_used;
     for (int b = threadIdx.x; b < P.B; b += RES_THREADS) P.total_len[b] = s_len[b] + s_new[b];
   }
-  // new entries of the block table
-  for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-    const int have = (int)(((long long)s_len[b] + P.bt - 1) / P.bt);
-    const int want = (int)(((long long)s_len[b] + s_new[b] + P.bt - 1) / P.bt);
-    for (int j = have + threadIdx.x; j < want; j += RES_THREADS)
-      P.block_table[(long long)b * P.max_blocks + j] = __ldg(P.free_blocks + s_first[b] - (j - have));
-  }
-  // slots: a new block's number comes from the stack, the last old block's
-  // from the table (whose entries before `have` this kernel does not write)
-  const long long slots = (long long)P.B * P.n;
-  for (long long e = (long long)blockIdx.x * RES_THREADS + threadIdx.x; e < slots;
-       e += (long long)gridDim.x * RES_THREADS) {
-    const int b = (int)(e / P.n), i = (int)(e - (long long)b * P.n);
-    int64_t slot = -1;
-    if (i < s_new[b]) {
-      const int pos = s_len[b] + i, j = pos / P.bt;
-      const int have = (int)(((long long)s_len[b] + P.bt - 1) / P.bt);
-      const int id = j < have ? __ldg(P.block_table + (long long)b * P.max_blocks + j)
-                              : __ldg(P.free_blocks + s_first[b] - (j - have));
-      if (id < 0)
-        report(P.err, MHA_ERR_INVALID_ARG);
-      else
-        slot = (int64_t)id * P.bt + (pos - j * P.bt);
+  // Slots, four of a sequence per thread. A new block's number comes from the
+  // stack, the last old block's from the table (whose entries before `have`
+  // this kernel does not write); the row that begins a new block, always one
+  // of the new rows, enters it in the table.
+  const unsigned quads = (P.n + 3) / 4, all = P.B * quads;
+  for (unsigned e = blockIdx.x * RES_THREADS + threadIdx.x; e < all; e += gridDim.x * RES_THREADS) {
+    const int b = (int)(e / quads), i0 = (int)(e - b * quads) * 4;
+    const int len = s_len[b], add = s_new[b], first = s_first[b];
+    const int have = (int)(((long long)len + P.bt - 1) / P.bt);
+    int32_t* row = P.block_table + (long long)b * P.max_blocks;
+    int64_t slot[4] = {-1, -1, -1, -1};
+    if (i0 < add) {
+      int j = (len + i0) / P.bt, at = len + i0 - j * P.bt;
+      int id = j < have ? __ldg(row + j) : __ldg(P.free_blocks + first - (j - have));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k >= add) break;
+        if (at == P.bt) {
+          at = 0;
+          ++j;
+          id = __ldg(P.free_blocks + first - (j - have));
+        }
+        if (at == 0) row[j] = id;
+        if (id < 0)
+          report(P.err, MHA_ERR_INVALID_ARG);
+        else
+          slot[k] = (int64_t)id * P.bt + at;
+        ++at;
+      }
     }
-    P.slot_map[e] = slot;
+    int64_t* out = P.slot_map + (long long)b * P.n + i0;
+    if (P.n % 2 == 0 && i0 + 3 < P.n) {  // 16-byte aligned
+      reinterpret_cast<longlong2*>(out)[0] = make_longlong2(slot[0], slot[1]);
+      reinterpret_cast<longlong2*>(out)[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k < P.n) out[k] = slot[k];
+    }
   }
 }
 
@@ -215,7 +229,11 @@ __global__ void __launch_bounds__(RES_THREADS) release_kernel(const __grid_const
 // exact ratio of the scales and rounded again, which changes only those that
 // fall below the smallest normal number, 2^-6.
 
-constexpr int APP_THREADS = 128;
+//
+// Bound: memory; each row is read once and its bytes are written once. A CTA
+// takes the rows of one block and head, of keys or of values, and keeps them in
+// registers between the maximum and the rounding (blocks of more than 32,768
+// elements are read a second time, from L2).
 
 struct AppendParams {
   const void* x[2];   // K, V: (B, h, n, d)
@@ -227,46 +245,50 @@ struct AppendParams {
   int B, h, n, bt, n_blocks;
 };
 
-__device__ __forceinline__ float block_max(float v, float* s) {
+// Sixteen consecutive elements as they are, and as fp32.
+template <typename T>
+struct Vec16 {
+  uint4 u[sizeof(T)];
+  __device__ __forceinline__ void load(const void* p) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = s[0];
-#pragma unroll
-  for (int w = 1; w < APP_THREADS / 32; ++w) v = fmaxf(v, s[w]);
-  return v;
-}
-
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < (int)sizeof(T); ++i) u[i] = __ldg(static_cast<const uint4*>(p) + i);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) {
+          v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+          v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+          v[4 * i + k] = __uint_as_float(w[k]);
+        }
+      }
+    }
+  }
+};
 
 // Two values as e4m3 (round to nearest even, beyond 448 to 448, NaN to NaN).
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&v)[8]) {
-  return make_uint2(pack_e4m3x2(v[0], v[1]) | pack_e4m3x2(v[2], v[3]) << 16,
-                    pack_e4m3x2(v[4], v[5]) | pack_e4m3x2(v[6], v[7]) << 16);
-}
-__device__ __forceinline__ void unpack_e4m3x8(uint2 u, float (&v)[8]) {
-  const uint32_t w[2] = {u.x, u.y};
+__device__ __forceinline__ uint4 pack_e4m3x16(const float (&v)[16]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i)
+    w[i] = pack_e4m3x2(v[4 * i], v[4 * i + 1]) | pack_e4m3x2(v[4 * i + 2], v[4 * i + 3]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack_e4m3x16(uint4 u, float (&v)[16]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
         (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3));
     const float2 f = __half22float2(h);
@@ -283,11 +305,27 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float((uint32_t)e << 23);
 }
 
+// v / s: a power of two's reciprocal is exact (2^127's is denormal, but exact
+// too), so the product is the quotient; a scale that the cache came with may
+// be any number.
+__device__ __forceinline__ void divide(float (&v)[16], float s) {
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
+    const float r = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] /= s;
+  }
+}
+
 // One CTA: the rows of one batch item that lie in one block of one head, of K
-// or of V. grid (parts, h, 2 B).
-template <typename T>
-__global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_constant__ AppendParams P) {
-  __shared__ float red[APP_THREADS / 32];
+// or of V. grid (parts, h, 2 B). HELD: vectors of 16 elements that a thread
+// keeps (0: none, the rows are read again).
+template <typename T, int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendParams P) {
+  __shared__ float red[THREADS / 32];
+  __shared__ int s_rows;
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int which = blockIdx.z & 1, b = blockIdx.z >> 1, head = blockIdx.y;
@@ -295,65 +333,113 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
   const int64_t first = __ldg(slots);
   if (first < 0) return;  // no new rows
   const int off = (int)(first % P.bt);
+  const int kept = blockIdx.x == 0 ? off : 0;  // rows that the block holds already
   const int row0 = blockIdx.x == 0 ? 0 : blockIdx.x * P.bt - off;  // first row of the part
   if (row0 >= P.n) return;
+  const int d = P.d[which], vecs = d / 16, most = min(P.bt - kept, P.n - row0);
+  const T* x = static_cast<const T*>(P.x[which]) + (((long long)b * P.h + head) * P.n + row0) * d;
+  // the rows, on their way while the slots are looked at
+  Vec16<T> v[HELD > 0 ? HELD : 1];
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      const int e = threadIdx.x + k * THREADS;
+      if (e < most * vecs) v[k].load(x + (long long)e * 16); else v[k].zero();
+    }
+  }
+  if (threadIdx.x == 0) s_rows = most;
   const int64_t slot0 = __ldg(slots + row0);
   if (slot0 < 0) return;  // past the item's last row
   const int64_t block = slot0 / P.bt;
-  const int kept = blockIdx.x == 0 ? off : 0;  // rows that the block holds already
-  const int rows = min(P.bt - kept, P.n - row0);
   if (block >= P.n_blocks || slot0 != block * P.bt + kept) {
     if (threadIdx.x == 0) report(P.err, MHA_ERR_INVALID_ARG);
     return;
   }
-  const int d = P.d[which], vecs = d / 8;
-  const T* x = static_cast<const T*>(P.x[which]) + (((long long)b * P.h + head) * P.n + row0) * d;
-  uint8_t* out = P.cache[which] + (block * P.h + head) * (long long)P.bt * d;
-  float* scale = P.scale[which] + block * P.h + head;
-
-  float amax = 0.f;
-  bool odd = false;
-  for (int e = threadIdx.x; e < rows * vecs; e += APP_THREADS) {
-    const int r = e / vecs;
+  __syncthreads();
+  // the rows up to the first whose slot does not follow
+  for (int r = threadIdx.x; r < most; r += THREADS) {
     const int64_t slot = __ldg(slots + row0 + r);
     if (slot != slot0 + r) {
-      odd |= slot >= 0;
-      continue;
-    }
-    float v[8];
-    load8(x + (long long)e * 8, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(v[i]);
-      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // finite values only
+      atomicMin(&s_rows, r);
+      if (slot >= 0) report(P.err, MHA_ERR_INVALID_ARG);
     }
   }
-  if (odd) report(P.err, MHA_ERR_INVALID_ARG);
+  __syncthreads();
+  const int count = s_rows * vecs;
+  uint8_t* out = P.cache[which] + (block * P.h + head) * (long long)P.bt * d;
+  float* scale = P.scale[which] + block * P.h + head;
   const float before = kept ? *scale : 0.f;
-  amax = block_max(amax, red);  // its barrier: every thread has read the old scale
+
+  float amax = 0.f;
+  auto take = [&](const Vec16<T>& u) {
+    float f[16];
+    u.get(f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = fabsf(f[i]);
+      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // finite values only
+    }
+  };
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (threadIdx.x + k * THREADS < count) take(v[k]);
+  } else {
+    for (int e = threadIdx.x; e < count; e += THREADS) {
+      v[0].load(x + (long long)e * 16);
+      take(v[0]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
+  __syncthreads();  // every thread has read the old scale, too
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
   float s = pow2_scale(amax);
   if (kept) s = fmaxf(s, before);
   if (threadIdx.x == 0) *scale = s;
   if (kept && s > before) {
     const float ratio = before / s;
-    for (int e = threadIdx.x; e < kept * vecs; e += APP_THREADS) {
-      uint2* p = reinterpret_cast<uint2*>(out) + e;
-      float v[8];
-      unpack_e4m3x8(*p, v);
+    for (int e = threadIdx.x; e < kept * vecs; e += THREADS) {
+      uint4* p = reinterpret_cast<uint4*>(out) + e;
+      float f[16];
+      unpack_e4m3x16(*p, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= ratio;
-      *p = pack_e4m3x8(v);
+      for (int i = 0; i < 16; ++i) f[i] *= ratio;
+      *p = pack_e4m3x16(f);
     }
   }
-  for (int e = threadIdx.x; e < rows * vecs; e += APP_THREADS) {
-    const int r = e / vecs;
-    if (__ldg(slots + row0 + r) != slot0 + r) continue;
-    float v[8];
-    load8(x + (long long)e * 8, v);
+  uint4* to = reinterpret_cast<uint4*>(out + (long long)kept * d);
+  auto put = [&](const Vec16<T>& u, int e) {
+    float f[16];
+    u.get(f);
+    divide(f, s);
+    to[e] = pack_e4m3x16(f);
+  };
+  if constexpr (HELD > 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
-    reinterpret_cast<uint2*>(out + (long long)kept * d)[e] = pack_e4m3x8(v);
+    for (int k = 0; k < HELD; ++k) {
+      const int e = threadIdx.x + k * THREADS;
+      if (e < count) put(v[k], e);
+    }
+  } else {
+    for (int e = threadIdx.x; e < count; e += THREADS) {
+      v[0].load(x + (long long)e * 16);
+      put(v[0], e);
+    }
   }
+}
+
+template <typename T>
+cudaError_t launch_append(const AppendParams& P, dim3 grid, cudaStream_t s) {
+  // the fewest threads whose registers hold a block's rows
+  const long long vecs = (long long)(P.n < P.bt ? P.n : P.bt) * (P.d[0] > P.d[1] ? P.d[0] : P.d[1]) / 16;
+  if (vecs <= 64) return launch_dependent(append_kernel<T, 64, 1>, grid, dim3(64), 0, s, P);
+  if (vecs <= 128 * 4) return launch_dependent(append_kernel<T, 128, 4>, grid, dim3(128), 0, s, P);
+  if (vecs <= 256 * 4) return launch_dependent(append_kernel<T, 256, 4>, grid, dim3(256), 0, s, P);
+  if (vecs <= 512 * 4) return launch_dependent(append_kernel<T, 512, 4>, grid, dim3(512), 0, s, P);
+  return launch_dependent(append_kernel<T, 512, 0>, grid, dim3(512), 0, s, P);
 }
 
 }  // namespace
@@ -367,8 +453,8 @@ mha_status cache_reserve(const ReserveArgs& a, bool release, cudaStream_t s) {
     const int grid = a.B < num_sms() ? a.B : num_sms();
     e = launch_dependent(release_kernel, dim3(grid), dim3(RES_THREADS), 0, s, P);
   } else {
-    // about 8 slots per thread, at most two CTAs per SM: each repeats the scan
-    long long grid = ((long long)a.B * a.n + 8 * RES_THREADS - 1) / (8 * RES_THREADS);
+    // four slots per thread, at most two CTAs per SM: each repeats the scan
+    long long grid = ((long long)a.B * ((a.n + 3) / 4) + RES_THREADS - 1) / RES_THREADS;
     if (grid > 2 * num_sms()) grid = 2 * num_sms();
     e = launch_dependent(reserve_kernel, dim3((unsigned)grid), dim3(RES_THREADS), 0, s, P);
   }
@@ -390,10 +476,8 @@ mha_status cache_append(const AppendArgs& a, mha_dtype dt, cudaStream_t s) {
                  a.n_blocks};
   const int parts = (int)(((long long)a.bt - 1 + a.n - 1) / a.bt) + 1;
   const dim3 grid(parts, a.h, 2 * a.B);
-  const cudaError_t e =
-      dt == MHA_DTYPE_F32
-          ? launch_dependent(append_kernel<float>, grid, dim3(APP_THREADS), 0, s, P)
-          : launch_dependent(append_kernel<__nv_bfloat16>, grid, dim3(APP_THREADS), 0, s, P);
+  const cudaError_t e = dt == MHA_DTYPE_F32 ? launch_append<float>(P, grid, s)
+                                            : launch_append<__nv_bfloat16>(P, grid, s);
   count_launch();
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }

@@ -315,7 +315,7 @@ mha_status check_pool(const ReserveArgs& a, bool release) {
   if (a.n_free_out == a.n_free || a.total_len == a.cached_len || a.total_len == a.new_len)
     return MHA_ERR_INVALID_ARG;
   if (a.B > MHA_MAX_PADDED_BATCH || a.bt > MHA_MAX_BLOCK_TOKENS ||
-      !fits(a.max_blocks, a.bt, 1))
+      !fits(a.max_blocks, a.bt, 1) || (!release && !fits(a.B, a.n, 1)))
     return MHA_ERR_UNSUPPORTED;
   return MHA_OK;
 }
@@ -731,10 +731,11 @@ mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V
   if (!dtype_ok(dt) || !isfinite(c)) return MHA_ERR_INVALID_ARG;
   if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > MHA_MAX_PADDED_BATCH)
     return MHA_ERR_UNSUPPORTED;
-  // keys of a sequence, 16-key groups of a batch, blocks of all heads, output
-  // rows: 32-bit counts
-  if (!fits(max_blocks, block_tokens, 1) || !fits(B, max_blocks, block_tokens / 16) ||
-      !fits(n_blocks, h_kv, 1) || !fits((long long)B, n_q, h))
+  // keys of a sequence, blocks of all heads, rows of Z, 16-key groups of all
+  // tiles of rows (and what tiles cost beside them): 32-bit counts
+  const long long rows = (long long)n_q * (h / h_kv), tiles = h_kv * ((rows + 15) / 16);
+  if (!fits(max_blocks, block_tokens, 1) || !fits(n_blocks, h_kv, 1) || !fits((long long)B, n_q, h) ||
+      !fits((long long)B * max_blocks, block_tokens / 16 + 8, tiles))
     return MHA_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(Z))
     return MHA_ERR_UNSUPPORTED;

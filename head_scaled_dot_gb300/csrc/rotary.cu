@@ -62,7 +62,7 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2
 // of N elements; interleaved pairing (2i, 2i + 1): one vector of N elements
 // holds N / 2 pairs (N = 1 when pairs cannot be read as one vector).
 template <typename T, int N, bool INTERLEAVED>
-__global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const __grid_constant__ RotaryParams P) {
+__global__ void __launch_bounds__(ROT_THREADS, 4) rotary_kernel(const __grid_constant__ RotaryParams P) {
   constexpr int NP = INTERLEAVED ? N / 2 : N;  // pairs per thread
   using V = Pack<T, N>;
   grid_dep_wait();
@@ -90,35 +90,60 @@ __global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const __grid_consta
   }
   // first element of the vector (of the second one: + P.pairs)
   const int col = !rotated ? 2 * P.pairs + (chunk - P.rot_chunks) * N : chunk * N;
+  // Heads in batches of HB, whose loads are all under way before the first
+  // store: an output may be its own input, so the compiler cannot move a load
+  // above the store before it. 64 bytes a thread; more, or a fourth CTA's
+  // registers taken away, is slower: 16,384 rows of 2 x 16 heads of 128 in bf16
+  // take 49 us so, 59 us head by head, 55 with two heads and any number of
+  // registers, 67 with four (a copy of the same bytes: 43).
+  constexpr int HB = INTERLEAVED ? 4 : 2;
   const int h0 = blockIdx.y * P.group, h1 = min(h0 + P.group, P.heads[0] + P.heads[1]);
-#pragma unroll 4
-  for (int hh = h0; hh < h1; ++hh) {
-    const int which = hh >= P.heads[0];
-    const int head = which ? hh - P.heads[0] : hh;
-    const long long at = (((long long)b * P.heads[which] + head) * P.T + t) * P.d + col;
-    const T* x = static_cast<const T*>(P.x[which]) + at;
-    T* y = static_cast<T*>(P.y[which]) + at;
-    V u = *reinterpret_cast<const V*>(x);
-    if (rotated) {
-      if constexpr (INTERLEAVED) {
+  const long long stride = (long long)P.T * P.d, in_head = (long long)t * P.d + col;
+  for (int hb = h0; hb < h1; hb += HB) {
+    V u[HB], w[INTERLEAVED ? 1 : HB];
+    auto place = [&](int hh, int& which) {
+      which = hh >= P.heads[0];
+      return ((long long)b * P.heads[which] + (which ? hh - P.heads[0] : hh)) * stride + in_head;
+    };
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const float p = to_f(u.v[2 * j]), q = to_f(u.v[2 * j + 1]);
-          from_f(u.v[2 * j], p * cs[j] - q * sn[j]);
-          from_f(u.v[2 * j + 1], p * sn[j] + q * cs[j]);
+    for (int k = 0; k < HB; ++k) {
+      if (hb + k < h1) {
+        int which;
+        const long long at = place(hb + k, which);
+        const T* x = static_cast<const T*>(P.x[which]) + at;
+        u[k] = *reinterpret_cast<const V*>(x);
+        if constexpr (!INTERLEAVED) {
+          if (rotated) w[k] = *reinterpret_cast<const V*>(x + P.pairs);
         }
-      } else {
-        V w = *reinterpret_cast<const V*>(x + P.pairs);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const float p = to_f(u.v[j]), q = to_f(w.v[j]);
-          from_f(u.v[j], p * cs[j] - q * sn[j]);
-          from_f(w.v[j], p * sn[j] + q * cs[j]);
-        }
-        *reinterpret_cast<V*>(y + P.pairs) = w;
       }
     }
-    *reinterpret_cast<V*>(y) = u;
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+      if (hb + k < h1) {
+        int which;
+        const long long at = place(hb + k, which);
+        T* y = static_cast<T*>(P.y[which]) + at;
+        if (rotated) {
+          if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const float p = to_f(u[k].v[2 * j]), q = to_f(u[k].v[2 * j + 1]);
+              from_f(u[k].v[2 * j], p * cs[j] - q * sn[j]);
+              from_f(u[k].v[2 * j + 1], p * sn[j] + q * cs[j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const float p = to_f(u[k].v[j]), q = to_f(w[k].v[j]);
+              from_f(u[k].v[j], p * cs[j] - q * sn[j]);
+              from_f(w[k].v[j], p * sn[j] + q * cs[j]);
+            }
+            *reinterpret_cast<V*>(y + P.pairs) = w[k];
+          }
+        }
+        *reinterpret_cast<V*>(y) = u[k];
+      }
+    }
   }
 }
 
@@ -131,8 +156,8 @@ cudaError_t launch(RotaryParams& P, bool interleaved, cudaStream_t s) {
     P.chunks += (P.d - 2 * P.pairs) / N;
   const long long threads = P.rows * P.chunks;
   const int heads = P.heads[0] + P.heads[1];
-  // as many heads per thread as leave every SM its threads
-  const long long want = (long long)num_sms() * 2048;
+  // as many heads per thread as leave every SM its threads (four CTAs' worth)
+  const long long want = (long long)num_sms() * 1024;
   long long groups = (want + threads - 1) / threads;
   if (groups > heads) groups = heads;
   P.group = (int)((heads + groups - 1) / groups);

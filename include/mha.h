@@ -512,9 +512,9 @@ MHA_API mha_status mha_cache_release(const int32_t* cached_len, const int32_t* f
  *   slot_map (B, n)   as mha_cache_reserve writes it: the rows of a batch item
  *                     that are written come first, in consecutive positions;
  *                     rows with slot -1 are not written. No two batch items
- *                     share a block. A row whose slot does not follow the row
- *                     before it is not written (MHA_ERR_INVALID_ARG in
- *                     dev_error)
+ *                     share a block. From a row on whose slot does not follow
+ *                     that of the row before it, the rows of its block are not
+ *                     written (MHA_ERR_INVALID_ARG in dev_error)
  *
  * A block's scale is the smallest power of two s (at least 2^-126) with
  * |x| / s <= 448 for all its rows, and every value is rounded once, to the
@@ -567,8 +567,9 @@ MHA_API size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_k
  *
  * MHA_ERR_INVALID_ARG for NULL pointers, non-positive sizes, h not a multiple
  * of h_kv, non-finite c; MHA_ERR_UNSUPPORTED for other head or block sizes
- * than above, B above MHA_MAX_PADDED_BATCH, more than 2^31 - 1 keys per
- * sequence, 16-key groups per batch or rows of Z, misaligned pointers;
+ * than above, B above MHA_MAX_PADDED_BATCH, misaligned pointers, or more than
+ * 2^31 - 1 keys per sequence, cache blocks of all heads, rows of Z, or 16-key
+ * groups for all key/value heads and tiles of 16 query rows of a batch;
  * MHA_ERR_WORKSPACE for a missing, misaligned or small workspace. Enqueues two
  * kernels.
  */

@@ -544,6 +544,21 @@ def test_attention_is_the_same_whatever_the_workspace_holds():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+@pytest.mark.parametrize("n_q,share", [(1, 1), (4, 4), (200, 4)])
+def test_calls_in_a_row_end_and_agree(n_q, share):
+    """Many groups per CTA, call after call without a wait between them: no
+    wait inside the kernel runs out, and every call gives the same bits."""
+    B, h_kv, L, bt = 2, 4, 6000, 64
+    cache = Cache(2 * -(-L // bt) + 1, h_kv, bt, 128, 128, 91)
+    table = ints(table_of([L, L - 77], bt, 2 * -(-L // bt) + 1, -(-L // bt), 8).tolist())
+    Q = torch.randn((B, h_kv * share, n_q, 128), device="cuda").bfloat16()
+    lens, err = ints([L, L - 77]), word()
+    out = [mha.attention_cache(Q, *cache.args, table, lens, 0.09, causal_tail=True, dev_error=err)
+           for _ in range(40)]
+    assert mha.get_device_error(err) == OK
+    assert all(torch.equal(z, out[0]) for z in out)
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 4 GB of keys: rows written to and read from its end."""
     n_blocks, h, bt, d_h, d_vh = 36000, 8, 64, 256, 16
