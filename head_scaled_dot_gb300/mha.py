@@ -7,6 +7,7 @@ fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -397,29 +398,41 @@ def attention_decode(Q, K, V, c, cache_len=None, causal_tail=False, out=None, wo
 CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _cuda(name, t, dtype, shape, device):
+def _cuda(name, t, dtype, shape, index):
     """The data pointer of a tensor that must be contiguous, of this type and
-    shape and on this device."""
-    if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError("%s: %s expected, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s: on %s, expected on %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s: must be contiguous" % name)
-    return t.data_ptr()
+    shape and on CUDA device `index`."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError("%s: contiguous %s of shape %s on cuda:%d expected, got %s%s of shape %s on %s"
+                     % (name, dtype, tuple(shape), index, "" if t.is_contiguous() else "strided ",
+                        t.dtype, tuple(t.shape), t.device))
 
 
-def _queue(device, stream):
-    """The stream handle of a call on `device`, which must be the current one:
-    kernels run on the current device."""
-    if device.type != "cuda":
-        raise ValueError("CUDA tensors expected, got a tensor on %s" % device)
-    if device.index != torch.cuda.current_device():
+def _cache_type(t):
+    """The element type of a cache tensor, which must be one of bytes."""
+    if t.dtype not in CACHE_DTYPES:
+        raise ValueError("cache: one of %s expected, got %s" % (CACHE_DTYPES, t.dtype))
+    return t.dtype
+
+
+# The current stream's handle of a device, without the stream object around it
+# (which takes longer to make than a small kernel runs).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _queue(t, stream):
+    """The device index of `t`, which must be the current device (kernels run
+    on it), and the handle of `stream` (None: the current one)."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("CUDA tensors expected, got a tensor on %s" % t.device)
+    if index != torch.cuda.current_device():
         raise ValueError("tensors on %s, but the current device is %d"
-                         % (device, torch.cuda.current_device()))
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+                         % (t.device, torch.cuda.current_device()))
+    if stream is not None:
+        return index, stream.cuda_stream
+    return index, (_raw_stream(index) if _raw_stream else torch.cuda.current_stream().cuda_stream)
 
 
 def _scratch(shape, dtype, device, stream):
@@ -437,8 +450,14 @@ def _dtype(t):
     return DTYPES[TORCH_DTYPES[t.dtype]]
 
 
-def _ints(values):
+@functools.lru_cache(maxsize=64)
+def _int_array(values):
     return (ctypes.c_int32 * len(values))(*values)
+
+
+def _ints(values):
+    """A host int32 array (read during the call only) of a list's values."""
+    return _int_array(tuple(values))
 
 
 def rotary_steps(sections, base=10000.0, per_axis=False, device="cuda"):
@@ -459,11 +478,11 @@ def rotary(Q, K, positions, steps, sections, interleaved=False, inverse=False, o
     may be (Q, K). Returns (Q_out, K_out)."""
     lib = load()
     B, h, T, d = Q.shape
-    dev, dt = Q.device, _dtype(Q)
-    s = _queue(dev, stream)
+    dt = _dtype(Q)
+    dev, s = _queue(Q, stream)
     if out is None:
-        out = (_scratch(Q.shape, Q.dtype, dev, stream),
-               None if K is None else _scratch(K.shape, K.dtype, dev, stream))
+        out = (_scratch(Q.shape, Q.dtype, Q.device, stream),
+               None if K is None else _scratch(K.shape, K.dtype, K.device, stream))
     Qo, Ko = out
     n_axes, h_kv, kp, kop = len(sections), 0, None, None
     if K is not None:
@@ -488,11 +507,11 @@ def cache_reserve(cached_len, new_len, free_blocks, n_free, block_table, block_t
     write into. Returns them."""
     lib = load()
     B, max_blocks = block_table.shape
-    dev, i32 = block_table.device, torch.int32
-    s = _queue(dev, stream)
+    i32, on = torch.int32, block_table.device
+    dev, s = _queue(block_table, stream)
     if out is None:
-        out = (_scratch((B,), i32, dev, stream), _scratch((B, n), torch.int64, dev, stream),
-               _scratch((1,), i32, dev, stream))
+        out = (_scratch((B,), i32, on, stream), _scratch((B, n), torch.int64, on, stream),
+               _scratch((1,), i32, on, stream))
     total_len, slot_map, n_free_out = out
     n_blocks = free_blocks.numel()
     st = lib.mha_cache_reserve(_cuda("cached_len", cached_len, i32, (B,), dev),
@@ -519,10 +538,10 @@ def cache_release(cached_len, finished, free_blocks, n_free, block_table, block_
     into. Returns them."""
     lib = load()
     B, max_blocks = block_table.shape
-    dev, i32 = block_table.device, torch.int32
-    s = _queue(dev, stream)
+    i32, on = torch.int32, block_table.device
+    dev, s = _queue(block_table, stream)
     if out is None:
-        out = (_scratch((B,), i32, dev, stream), _scratch((1,), i32, dev, stream))
+        out = (_scratch((B,), i32, on, stream), _scratch((1,), i32, on, stream))
     total_len, n_free_out = out
     n_blocks = free_blocks.numel()
     st = lib.mha_cache_release(_cuda("cached_len", cached_len, i32, (B,), dev),
@@ -546,13 +565,13 @@ def cache_append(K, V, slot_map, K_cache, V_cache, K_scale, V_scale, dev_error=N
     B, h, n, d_h = K.shape
     d_vh = V.shape[3]
     n_blocks, bt = K_cache.shape[0], K_cache.shape[2]
-    dev, dt, f32 = K.device, _dtype(K), torch.float32
-    s = _queue(dev, stream)
+    dt, f32, byte = _dtype(K), torch.float32, _cache_type(K_cache)
+    dev, s = _queue(K, stream)
     st = lib.mha_cache_append(_cuda("K", K, K.dtype, (B, h, n, d_h), dev),
                               _cuda("V", V, K.dtype, (B, h, n, d_vh), dev),
                               _cuda("slot_map", slot_map, torch.int64, (B, n), dev),
-                              _cuda("K_cache", K_cache, CACHE_DTYPES, (n_blocks, h, bt, d_h), dev),
-                              _cuda("V_cache", V_cache, CACHE_DTYPES, (n_blocks, h, bt, d_vh), dev),
+                              _cuda("K_cache", K_cache, byte, (n_blocks, h, bt, d_h), dev),
+                              _cuda("V_cache", V_cache, byte, (n_blocks, h, bt, d_vh), dev),
                               _cuda("K_scale", K_scale, f32, (n_blocks, h), dev),
                               _cuda("V_scale", V_scale, f32, (n_blocks, h), dev), B, n, h, d_h,
                               d_vh, n_blocks, bt, dt, _word(dev_error, dev), s)
@@ -574,19 +593,19 @@ def attention_cache(Q, K_cache, V_cache, K_scale, V_scale, block_table, total_le
     B, h, n_q, d_h = Q.shape
     n_blocks, h_kv, bt, d_vh = V_cache.shape
     max_blocks = block_table.shape[1]
-    dev, dt, f32, i32 = Q.device, _dtype(Q), torch.float32, torch.int32
-    s = _queue(dev, stream)
+    dt, f32, i32, byte = _dtype(Q), torch.float32, torch.int32, _cache_type(K_cache)
+    dev, s = _queue(Q, stream)
     if out is None:
-        out = _scratch((B, n_q, h * d_vh), Q.dtype, dev, stream)
+        out = _scratch((B, n_q, h * d_vh), Q.dtype, Q.device, stream)
     if workspace is None:
         nbytes = attention_cache_workspace_size(B, n_q, h, h_kv, d_h, d_vh)
-        workspace = _scratch((nbytes,), torch.uint8, dev, stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: contiguous, on %s" % dev)
+        workspace = _scratch((nbytes,), torch.uint8, Q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous, on %s" % Q.device)
     st = lib.mha_attention_cache(
         _cuda("Q", Q, Q.dtype, Q.shape, dev),
-        _cuda("K_cache", K_cache, CACHE_DTYPES, (n_blocks, h_kv, bt, d_h), dev),
-        _cuda("V_cache", V_cache, CACHE_DTYPES, (n_blocks, h_kv, bt, d_vh), dev),
+        _cuda("K_cache", K_cache, byte, (n_blocks, h_kv, bt, d_h), dev),
+        _cuda("V_cache", V_cache, byte, (n_blocks, h_kv, bt, d_vh), dev),
         _cuda("K_scale", K_scale, f32, (n_blocks, h_kv), dev),
         _cuda("V_scale", V_scale, f32, (n_blocks, h_kv), dev),
         _cuda("block_table", block_table, i32, (B, max_blocks), dev),

@@ -184,8 +184,10 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(lib):
     with pytest.raises(ValueError):
         mha.rotary(Q.half(), None, pos, steps, [32])
     with pytest.raises(ValueError):
-        mha._cuda("x", Q.transpose(1, 3), torch.bfloat16, (1, 64, 1, 2), Q.device)
+        mha.rotary(Q.transpose(1, 3), None, pos, steps, [32])
+    for dtype, shape in [(torch.float32, Q.shape), (torch.bfloat16, (1, 2, 1, 32)),
+                         (torch.bfloat16, Q.shape)]:  # the last is on the CPU
+        with pytest.raises(ValueError):
+            mha._cuda("x", Q, dtype, shape, 0)
     with pytest.raises(ValueError):
-        mha._cuda("x", Q, torch.float32, Q.shape, Q.device)
-    with pytest.raises(ValueError):
-        mha._cuda("x", Q, torch.bfloat16, (1, 2, 1, 32), Q.device)
+        mha._cache_type(Q)
