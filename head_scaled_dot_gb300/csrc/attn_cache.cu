@@ -661,22 +661,24 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   }
 }
 
-// One output row per CTA: zeros where it sees no key, else the merge of its
-// tile's pieces in order, unless a single warp had the tile whole and wrote it.
-template <int D, typename T>
+// An output row: zeros where it sees no key, else the merge of its tile's
+// pieces in order, unless a single range had the tile whole and wrote it. The
+// CTA's groups of threads take a row each (ROWS), or a row's pieces in turn.
+template <int D, typename T, bool ROWS>
 __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_constant__ CacheAttnParams P) {
   constexpr int CT = D / 4;              // threads across the columns, 4 each
-  constexpr int PG = CM_THREADS / CT;    // pieces at a time
+  constexpr int PG = CM_THREADS / CT;    // rows or pieces at a time
   __shared__ float sm[PG][2];
   __shared__ __align__(16) float sz[PG][D];
+  const int col = threadIdx.x % CT * 4, pg = threadIdx.x / CT;
   grid_dep_wait();
-  const int head = blockIdx.x % P.h;
-  const long long bi = blockIdx.x / P.h;
+  const long long at = ROWS ? (long long)blockIdx.x * PG + pg : blockIdx.x, bi = at / P.h;
+  if (bi >= (long long)P.B * P.n_q) return;
+  const int head = (int)(at - bi * P.h);
   const int i = (int)(bi % P.n_q), b = (int)(bi / P.n_q);
   const int kv = head / P.share, r = i * P.share + head % P.share;
   const int pr = kv * P.tiles + r / P.tile_rows, row = r % P.tile_rows;
   const int ng = P.first[b + 1] - P.first[b];
-  const int col = threadIdx.x % CT * 4, pg = threadIdx.x / CT;
   T* out = static_cast<T*>(P.Z) + (bi * P.h + head) * P.d_vh + col;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
     const float* ml = P.part;
     const float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows;
 #pragma unroll 2
-    for (int w = w0 + pg; w <= w1; w += PG) {
+    for (int w = w0 + (ROWS ? 0 : pg); w <= w1; w += ROWS ? 1 : PG) {
       // its units [u, v) of the costs, as the tile's groups
       const int u = w * ranges.per + min(w, ranges.more) - cost;
       const int v1 = u + ranges.per + (w < ranges.more ? 1 : 0);
@@ -713,26 +715,29 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
       m = mn;
     }
   }
-  if (threadIdx.x % CT == 0) {
-    sm[pg][0] = m;
-    sm[pg][1] = l;
-  }
-  *reinterpret_cast<float4*>(&sz[pg][col]) = acc;
-  __syncthreads();
-  if (pg != 0 || col >= P.d_vh) return;
+  if constexpr (!ROWS) {
+    if (threadIdx.x % CT == 0) {
+      sm[pg][0] = m;
+      sm[pg][1] = l;
+    }
+    *reinterpret_cast<float4*>(&sz[pg][col]) = acc;
+    __syncthreads();
+    if (pg != 0) return;
 #pragma unroll
-  for (int k = 1; k < PG; ++k) {
-    const float mw = sm[k][0];
-    if (mw == -INFINITY && sm[k][1] == 0.f) continue;
-    const float mn = fmaxf(m, mw);
-    const float x = m == mn ? 1.f : exp2f(m - mn), y = mw == mn ? 1.f : exp2f(mw - mn);
-    acc.x = acc.x * x + sz[k][col] * y;
-    acc.y = acc.y * x + sz[k][col + 1] * y;
-    acc.z = acc.z * x + sz[k][col + 2] * y;
-    acc.w = acc.w * x + sz[k][col + 3] * y;
-    l = l * x + sm[k][1] * y;
-    m = mn;
+    for (int k = 1; k < PG; ++k) {
+      const float mw = sm[k][0];
+      if (mw == -INFINITY && sm[k][1] == 0.f) continue;
+      const float mn = fmaxf(m, mw);
+      const float x = m == mn ? 1.f : exp2f(m - mn), y = mw == mn ? 1.f : exp2f(mw - mn);
+      acc.x = acc.x * x + sz[k][col] * y;
+      acc.y = acc.y * x + sz[k][col + 1] * y;
+      acc.z = acc.z * x + sz[k][col + 2] * y;
+      acc.w = acc.w * x + sz[k][col + 3] * y;
+      l = l * x + sm[k][1] * y;
+      m = mn;
+    }
   }
+  if (col >= P.d_vh) return;
   const bool none = i >= it.fresh || l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
   const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
@@ -759,12 +764,21 @@ mha_status launch(CacheAttnParams& P, cudaStream_t s) {
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 
+template <int D, typename T>
+cudaError_t launch_merge_columns(const CacheAttnParams& P, cudaStream_t s) {
+  const long long rows = (long long)P.B * P.n_q * P.h;
+  // With four pieces a tile and more they are read at a time.
+  if (P.ranges >= 4ll * P.B * P.h_kv * P.tiles)
+    return launch_dependent(cache_merge_kernel<D, T, false>, dim3((unsigned)rows), dim3(CM_THREADS), 0, s, P);
+  constexpr int PER = CM_THREADS / (D / 4);
+  return launch_dependent(cache_merge_kernel<D, T, true>, dim3((unsigned)((rows + PER - 1) / PER)),
+                          dim3(CM_THREADS), 0, s, P);
+}
 template <typename T>
 cudaError_t launch_merge(const CacheAttnParams& P, cudaStream_t s) {
-  const dim3 grid((unsigned)((long long)P.B * P.n_q * P.h)), block(CM_THREADS);
-  if (P.d_vh <= 64) return launch_dependent(cache_merge_kernel<64, T>, grid, block, 0, s, P);
-  if (P.d_vh <= 128) return launch_dependent(cache_merge_kernel<128, T>, grid, block, 0, s, P);
-  return launch_dependent(cache_merge_kernel<256, T>, grid, block, 0, s, P);
+  if (P.d_vh <= 64) return launch_merge_columns<64, T>(P, s);
+  if (P.d_vh <= 128) return launch_merge_columns<128, T>(P, s);
+  return launch_merge_columns<256, T>(P, s);
 }
 
 // The tensor-core kernel takes bf16 queries and head sizes up to 128: its
@@ -800,7 +814,7 @@ bool make_cache_maps(CacheAttnParams& P, int box_rows, int width) {
 size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_h, int d_vh) {
   const long long rows = (long long)n_q * (h / h_kv);
   const size_t few = (size_t)CA_MAX_CTAS * CA_WARPS * (rows < 16 ? rows : 16);
-  const size_t many = (size_t)CA_MAX_CTAS * (rows < 128 ? rows : 128);
+  const size_t many = (size_t)CA_MAX_CTAS * (rows < 256 ? rows : 256);
   const size_t slots = 2 * (many > few ? many : few);
   (void)d_h;
   return CA_HEADER + slots * (2 + (size_t)d_vh) * sizeof(float);
@@ -836,7 +850,7 @@ mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s)
   const int rows = a.n_q * P.share;
   const bool tc = on_tensor_cores(dt, a.d_h, a.d_vh);
   // up to 16 rows a tile of 16 (the cache is streamed once), else 128
-  P.tile_rows = tc && rows > 16 ? 128 : 16;
+  P.tile_rows = !tc || rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   P.tiles = (rows + P.tile_rows - 1) / P.tile_rows;
   P.slot_rows = rows < P.tile_rows ? rows : P.tile_rows;
   if (tc) return launch_cache_attention_tc(P, s);

@@ -49,6 +49,7 @@ constexpr int SIDE = KEYS * ROW;        // one side of a stage
 constexpr int STAGE = 2 * SIDE;
 constexpr float RAISE = 1.75f;          // a weight is at most 2^1.75 ...
 constexpr float UNIT = 128.f;           // ... times this: e4m3's largest is 448 > 2^8.75
+constexpr float MANY_RAISE = 8.f;       // many rows: fp16 weights, at most 2^8 times UNIT
 constexpr float HEADROOM = 1.f;         // few rows: references are set above the scores seen
 constexpr float NOTHING = -3e38f;       // a row's reference before its first key; finite, so that
                                         // a masked score's distance from it is -inf too
@@ -71,17 +72,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same with A in tensor memory, four elements per column.
-__device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -179,6 +169,12 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Barrier that says whether any of its threads passed true.
 __device__ __forceinline__ bool named_any(int id, int threads, bool v) {
   uint32_t r;
@@ -270,10 +266,11 @@ static __device__ __noinline__ void mend_values(uint32_t src, int row, bool seen
 // Warp 0 fills the ring with the key tiles of the groups from lc on, warp 2 with the value tiles and the scales, each walking the groups for itself. A
 // stage is full after an arrival of each for its tiles, one for the scales, and
 // the tiles' bytes.
-template <int NS>
+template <int NS, int NM>
 __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first,
                                           const int* totals, int unit, Cursor lc, int steps,
-                                          uint32_t stages, Meta* metas, uint64_t* full, uint64_t* empty, const WaitCtl& ctl) {
+                                          uint32_t stages, Meta* metas, uint64_t* full, uint64_t* there_meta,
+                                          uint64_t* empty, const WaitCtl& ctl) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // A lane has one box of a tile: its entry j of the block table and its row in
   // that block, moved on by 128 keys a step; warp 2's first eight lanes have 16
@@ -342,7 +339,8 @@ __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* f
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
       }
-      Meta* m = metas + stage;
+      const int at = NM == NS ? stage : n % NM;
+      Meta* m = metas + at;
       if (lane < 8) {
         m->ks[lane] = ks;
         m->vs[lane] = vs;
@@ -353,7 +351,7 @@ __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* f
         m->single = !(least < 0.25f * top);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + stage);
+      if (lane == 0) mbar_arrive(there_meta + at);
     }
     if (++stage == NS) {
       stage = 0;
@@ -484,7 +482,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, empty, ctl);
+    fill_ring<F::STAGES, F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, full,
+                                    empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- scores ----
     // Two threads issue the products, one the scores and one the value
@@ -932,27 +931,72 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 // ---------------------------------------------------------------------------
 
 struct Many {
-  static constexpr int SOFTMAX_WARPS = 8;
-  static constexpr int THREADS = 128 + 32 * SOFTMAX_WARPS;
-  static constexpr int STAGES = 4;
-  static constexpr int ROWS = 128;
-  static constexpr int PIECES = 2;                 // hi and lo of Q and of P
-  static constexpr int SUBS = 4;                   // groups of 16 keys per lane
-  static constexpr int OPERAND = 128 * ROW;        // 128 operand rows of e4m3
+  static constexpr int CONVERT_WARPS = 4, SOFTMAX_WARPS = 8;
+  static constexpr int CONVERT_AT = 128, SOFTMAX_AT = CONVERT_AT + 32 * CONVERT_WARPS;  // first threads
+  static constexpr int THREADS = SOFTMAX_AT + 32 * SOFTMAX_WARPS;
+  static constexpr int STAGES = 2;
+  static constexpr int METAS = 8;                  // scales outlive the bytes: the softmax reads them
+  static constexpr int ROWS = 128;                 // query rows of a slot
+  static constexpr int PANEL = 128 * ROW;          // 128 rows of 64 fp16 numbers
+  static constexpr int OPERAND = 2 * PANEL;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int S_COL = 0;                  // two score tiles of 128 columns; the weights over them
-  static constexpr int Z_COL = 256;                // hi's z, and lo's at Z_COL + 128
+  static constexpr int S_COL = 0;                  // a slot's scores, 128 columns; its weights over them
+  static constexpr int Z_COL = 256;                // a slot's z, 128 columns
   // shared memory
-  static constexpr int Q_AT = STAGES * STAGE;
-  static constexpr int META_AT = Q_AT + PIECES * OPERAND;
-  static constexpr int NAN_AT = META_AT + STAGES * (int)sizeof(Meta);
-  static constexpr int LIM_AT = NAN_AT + ROWS * 16;
-  static constexpr int QF_AT = LIM_AT + ROWS * 4;
-  static constexpr int FIRST_AT = QF_AT + ROWS * 4;
+  static constexpr int KEY_AT = STAGES * STAGE;    // the group's keys as fp16
+  static constexpr int VALUE_AT = KEY_AT + OPERAND;
+  static constexpr int Q_AT = VALUE_AT + OPERAND;  // a slot's queries
+  static constexpr int META_AT = Q_AT + 2 * OPERAND;
+  static constexpr int NAN_AT = META_AT + METAS * (int)sizeof(Meta);
+  static constexpr int LIM_AT = NAN_AT + 2 * ROWS * 16;
+  static constexpr int QF_AT = LIM_AT + 2 * ROWS * 4;
+  static constexpr int FIRST_AT = QF_AT + 2 * ROWS * 4;
   static constexpr int TOTAL_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
   static constexpr int BAR_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
-  static constexpr int SMEM = 1024 + BAR_AT + 256;
+  static constexpr int SMEM = 1024 + BAR_AT + 288;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
+
+// Instruction descriptor of kind f16: fp16 A and B, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The first and last new row of a tile, and what their rows see: keys up to
+// lim_all by every row (that sees any), none past lim_any by any row.
+struct TileLimits {
+  int lim_all, lim_any;
+  __device__ __forceinline__ TileLimits(const CacheAttnParams& P, const Item& it, int rt) {
+    const int rows = P.n_q * P.share, i0 = rt * P.tile_rows / P.share;
+    const int i1 = min((min(rows, (rt + 1) * P.tile_rows) - 1) / P.share, it.fresh - 1);
+    const int back = it.total - it.fresh;
+    lim_any = i1 < i0 ? -1 : P.causal_tail ? back + i1 : it.total - 1;
+    lim_all = P.causal_tail ? max(0, back + i0) : it.total - 1;
+  }
+};
+
+// What a softmax thread keeps of a query row, per slot.
+struct RowState {
+  float qf, m, l, vref, vtop;
+  int limit;       // keys up to here are seen
+  uint32_t jobs;   // score tiles so far
+  uint32_t prods;  // value products so far
+  bool fresh;      // no key of this tile yet: z holds nothing
+};
+
+// Half a tile (8 pieces of 16 bytes a thread) of e4m3 numbers from a stage as
+// fp16 into registers, and from there into the operand. A quarter of a warp
+// takes rows r and r + 4 and half their columns, and one of the two rows stores
+// its 16-byte pieces in the other order: no two of its lanes meet on a bank,
+// neither reading nor writing.
+__device__ __forceinline__ void read_piece(uint32_t src, int i, int row, int col, bool odd, uint4& a, uint4& b) {
+  const int r = row + 8 * (i >> 1), c = col + 4 * (i & 1);
+  const uint4 u = lds128(src + swz(r, c));
+  const uint32_t x0 = odd ? u.z : u.x, x1 = odd ? u.w : u.y, y0 = odd ? u.x : u.z, y1 = odd ? u.y : u.w;
+  a = make_uint4(e4m3_lo(x0), e4m3_hi(x0), e4m3_lo(x1), e4m3_hi(x1));
+  b = make_uint4(e4m3_lo(y0), e4m3_hi(y0), e4m3_lo(y1), e4m3_hi(y1));
+}
 
 __global__ void __launch_bounds__(Many::THREADS, 1)
     cache_attention_many_kernel(const __grid_constant__ CacheAttnParams P) {
@@ -962,34 +1006,56 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta* metas = reinterpret_cast<Meta*>(smem + F::META_AT);
+  uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
+  int* lim_s = reinterpret_cast<int*>(smem + F::LIM_AT);
+  float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
   int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
   int* totals = reinterpret_cast<int*>(smem + F::TOTAL_AT);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [F::STAGES] tiles and scales there
-  uint64_t* empty = full + F::STAGES;    // [F::STAGES] both products done
-  uint64_t* s_full = empty + F::STAGES;  // [2] scores there
-  uint64_t* q_full = s_full + 2;      // the tile's queries there
-  uint64_t* p_full = q_full + 1;      // [2] weights there
-  uint64_t* p_free = p_full + 2;      // value product done
-  uint64_t* done = p_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [STAGES] bytes there
+  uint64_t* empty = full + F::STAGES;    // [STAGES] bytes read
+  uint64_t* meta_full = empty + F::STAGES;  // [METAS] scales there
+  // A group's keys and values as fp16, there and no longer needed: even and
+  // odd groups have barriers of their own, so that a role that takes every
+  // second group only (one slot's) meets each phase of its barrier.
+  uint64_t* k_full = meta_full + F::METAS;
+  uint64_t* k_free = k_full + 2;
+  uint64_t* v_full = k_free + 2;
+  uint64_t* v_free = v_full + 2;
+  uint64_t* s_full = v_free + 2;      // [2 slots] scores there
+  uint64_t* p_full = s_full + 2;      // [2 slots] weights there
+  uint64_t* z_full = p_full + 2;      // [2 slots] value product done
+  uint64_t* q_full = z_full + 2;      // [2 slots] the tile's queries there
+  uint64_t* tile_full = q_full + 2;   // the tile's limits there
+  uint64_t* mended = tile_full + 1;
+  uint64_t* done = mended + 1;        // [2 issuing threads]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   __shared__ int warp_sums[F::THREADS / 32];
   __shared__ int abort_flag;
   __shared__ Cursor start;
   __shared__ int bounds[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // both slots take every group (two tiles of 128 rows), or turns (one tile)
+  const bool pair = P.tile_rows > F::ROWS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < F::STAGES; ++s) {
-      mbar_init(full + s, 3);  // key tiles, value tiles, scales
-      mbar_init(empty + s, 1);
+      mbar_init(full + s, 2);  // key tiles, value tiles
+      mbar_init(empty + s, F::CONVERT_WARPS);
     }
+    for (int s = 0; s < F::METAS; ++s) mbar_init(meta_full + s, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full + s, F::CONVERT_WARPS);
+      mbar_init(v_full + s, F::CONVERT_WARPS);
+      mbar_init(k_free + s, pair ? 2 : 1);
+      mbar_init(v_free + s, pair ? 2 : 1);
       mbar_init(s_full + s, 1);
       mbar_init(p_full + s, F::SOFTMAX_WARPS);
+      mbar_init(z_full + s, 1);
+      mbar_init(q_full + s, F::SOFTMAX_WARPS);
+      mbar_init(done + s, 1);
     }
-    mbar_init(q_full, F::SOFTMAX_WARPS);
-    mbar_init(p_free, 1);
-    mbar_init(done, 1);
+    mbar_init(tile_full, F::SOFTMAX_WARPS);
+    mbar_init(mended, F::CONVERT_WARPS);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.map_k);
@@ -1020,365 +1086,462 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   const int unit = P.h_kv * P.tiles, steps = bounds[1] - bounds[0];
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
-  if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, empty, ctl);
-  } else if (steps > 0 && warp == 1 && lane == 0) {
-    // ---- products ----
-    constexpr uint32_t idesc_s = idesc_e4m3_f32(128, KEYS, 0, 0);
-    const uint32_t idesc_z = idesc_e4m3_f32(128, P.d_vh, 0, 1);
-    const int slices = (P.d_h + 31) / 32;
-    const uint32_t base = smem_u32(smem);
-    const uint64_t q_desc = sdesc_sw128(base + F::Q_AT, 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(base, 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(base + SIDE, 16384, 1024);
-    Cursor cc = start;
-    bool ok = true, begins = true;
-    int tile = 0;
-    uint32_t pv = 0, pv_other = 0;  // value products of groups like this one (even or odd), of the others
-    auto issue_s = [&](int n) {
-      const int stage = n % F::STAGES, b = n & 1;
-      // The scores go over the weights of group n - 2, whose value product is
-      // ahead of them in this thread's order.
-      ok = ok && cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t kd = k_desc + (uint64_t)(stage * STAGE >> 4);
+  if (warp < F::CONVERT_AT / 32) {
+    if (steps > 0 && (warp == 0 || warp == 2)) {
+      fill_ring<F::STAGES, F::METAS>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full,
+                                     meta_full, empty, ctl);
+    } else if (steps > 0 && lane == 0) {
+      // ---- products of slot t ----
+      const int t = warp >> 1;
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, KEYS, 0, 0);
+      const uint32_t idesc_z = idesc_f16_f32(128, P.d_vh, 0, 1);
+      const int panels = P.d_h > 64 ? 2 : 1;
+      const uint32_t base = smem_u32(smem);
+      const uint64_t q_desc = sdesc_sw128(base + F::Q_AT + t * F::OPERAND, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(base + F::KEY_AT, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + F::VALUE_AT, F::PANEL, 1024);
+      const uint32_t s_tmem = tmem + F::S_COL + t * 128, z_tmem = tmem + F::Z_COL + t * 128;
+      Cursor cc = start;
+      bool ok = true, fresh = true;
+      uint32_t tile = 0, pv = 0;
+      for (int n = 0; n < steps; ++n) {
+        if (pair || (n & 1) == t) {
+          const uint32_t par = (n >> 1) & 1;
+          if (fresh) ok = cache_wait(q_full + t, tile++ & 1, ctl);
+          ok = ok && cache_wait(k_full + (n & 1), par, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          // The scores go over the weights of the slot's last group, whose
+          // value product is ahead of them in this thread's order.
+          // Zeros past d_h on both sides: whole panels of 64 columns. (A loop,
+          // not a branch around half of the products: compiled to predicated
+          // ones, those gave wrong sums.)
+#pragma unroll 1
+          for (int panel = 0; panel < panels; ++panel) {
+            const uint64_t at = (uint64_t)(panel * F::PANEL >> 4);
 #pragma unroll
-      for (int p = 0; p < F::PIECES; ++p) {
-        for (int k = 0; k < slices; ++k)
-          umma_f8(tmem + F::S_COL + b * KEYS, q_desc + (uint64_t)((p * F::OPERAND + k * 32) >> 4),
-                  kd + (uint64_t)(k * 32 >> 4), idesc_s, p + k > 0);
+            for (int k = 0; k < 4; ++k)
+              umma_ss(s_tmem, q_desc + at + (uint64_t)(k * 32 >> 4), k_desc + at + (uint64_t)(k * 32 >> 4),
+                      idesc_s, panel + k > 0);
+          }
+          umma_commit(s_full + t);
+          umma_commit(k_free + (n & 1));
+          ok = cache_wait(v_full + (n & 1), par, ctl);
+          const Meta* m = metas + n % F::METAS;
+          uint32_t todo = m->single ? 0u : m->found;
+          do {
+            if (todo) {
+              float top;
+              todo &= ~take_of(m, todo, top);
+            }
+            ok = ok && cache_wait(p_full + t, pv++ & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < KEYS / 16; ++k)
+              umma_ts(z_tmem, s_tmem + k * 8, v_desc + (uint64_t)(k * 16 * ROW >> 4), idesc_z, !fresh || k > 0);
+            umma_commit(z_full + t);
+            fresh = false;
+          } while (todo);
+          if (!ok) break;
+          umma_commit(v_free + (n & 1));
+        }
+        if (advance(cc, first, P.B, unit)) fresh = true;
       }
-      umma_commit(s_full + b);
-    };
-    for (int n = 0; ok && n < steps; ++n) {
+      umma_commit(done + t);  // the products in flight end before tensor memory is given back
+      wait_in_flight(done + t, 0);
+    }
+  } else if (warp < F::SOFTMAX_AT / 32) {
+    // ---- e4m3 to fp16 ----
+    // (After a wait that gave up the work goes on without waiting: nothing
+    // else here can block.)
+    const int tid = threadIdx.x - F::CONVERT_AT;
+    const int row = tid / 32 * 32 + (lane >> 3) + (lane & 4), col = lane & 3;
+    const bool odd = (lane & 4) != 0;
+    const uint32_t base = smem_u32(smem);
+    Cursor cc = start;
+    bool begins = true, waited = false;
+    uint32_t tile = 0, mends = 0;
+    int lim_all = 0, lim_any = -1;
+    for (int n = 0; n < steps; ++n) {
       const int stage = n % F::STAGES;
+      const uint32_t last = (n - 1) & 1, last_par = ((n - 1) >> 1) & 1;
       const bool ends = cc.gi == cc.ng - 1 || n == steps - 1;
       if (begins) {
-        ok = cache_wait(q_full, tile & 1, ctl);
-        ++tile;
-        issue_s(n);
+        bool bad;
+        const TileLimits lim(P, item_of(P, cc.b, bad), cc.pr % P.tiles);
+        lim_all = lim.lim_all;
+        lim_any = lim.lim_any;
+        waited = false;
       }
-      if (!ends) issue_s(n + 1);
-      if (!ok) break;
-      const Meta* m = metas + stage;
-      uint32_t todo = m->single ? 0u : m->found;
-      bool fresh = begins;
-      do {
-        if (todo) {
-          float top;
-          todo &= ~take_of(m, todo, top);
+      cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
+      cache_wait(meta_full + n % F::METAS, (n / F::METAS) & 1, ctl);
+      __syncwarp();
+      const int kb = cc.gi * KEYS;
+      const uint32_t found = metas[n % F::METAS].found;
+      const bool masked = kb + KEYS - 1 > lim_all || found != 0xffu;
+      if ((masked || ends) && !waited) {  // (each of the barrier's phases is met)
+        cache_wait(tile_full, tile++ & 1, ctl);
+        waited = true;
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        const uint32_t src = base + stage * STAGE + side * SIDE;
+        if (side && masked) {
+          mend_values(src, tid, (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, P.tile_rows, lim_s,
+                      nan_map);
+          fence_async_shared();  // the next bytes come by TMA
+          __syncwarp();
+          if (lane == 0) mbar_arrive(mended);
+          cache_wait(mended, mends++ & 1, ctl);
+          __syncwarp();
         }
-        if (!cache_wait(p_full + (n & 1), pv & 1, ctl)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t vd = v_desc + (uint64_t)(stage * STAGE >> 4);
+        uint4 a[8], b[8];
 #pragma unroll
-        for (int p = 0; p < F::PIECES; ++p) {
+        for (int i = 0; i < 8; ++i) read_piece(src, i, row, col, odd, a[i], b[i]);
+        __syncwarp();
+        if (side && lane == 0) mbar_arrive(empty + stage);
+        if (n > 0) cache_wait((side ? v_free : k_free) + last, last_par, ctl);
+        __syncwarp();
+        const uint32_t dst = base + (side ? F::VALUE_AT : F::KEY_AT);
 #pragma unroll
-          for (int k = 0; k < KEYS / 32; ++k)
-            umma_f8_ts(tmem + F::Z_COL + p * 128, tmem + F::S_COL + (n & 1) * KEYS + p * 32 + k * 8,
-                       vd + (uint64_t)(k * 32 * ROW >> 4), idesc_z, !fresh || k > 0);
+        for (int i = 0; i < 8; ++i) {
+          const int r = row + 8 * (i >> 1);
+          const uint32_t to = dst + (i & 1) * F::PANEL;
+          sts128(to + swz(r, 2 * col + (odd ? 1 : 0)), a[i]);
+          sts128(to + swz(r, 2 * col + (odd ? 0 : 1)), b[i]);
         }
-        umma_commit(p_free);
-        fresh = false;
-        ++pv;
-      } while (todo);
-      if (!ok) break;
-      umma_commit(empty + stage);
-      const uint32_t other = pv;
-      pv = pv_other;
-      pv_other = other;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive((side ? v_full : k_full) + (n & 1));
+      }
       begins = ends;
       advance(cc, first, P.B, unit);
     }
-    umma_commit(done);  // the products in flight end before tensor memory is given back
-    wait_in_flight(done, 0);
-  } else if (steps > 0 && warp >= 4) {
+  } else {
     // ---- softmax ----
-    // A warp has 16 rows: lane i < 16 holds the first 64 keys of row i, lane
-    // i + 16 the others.
-    const int q = warp & 3, hh = (warp - 4) >> 2, half = lane >> 4;
-    const int tid = threadIdx.x - 128;
+    // A warp has 16 rows of each slot: lane i < 16 holds the first 64 keys of
+    // row i, lane i + 16 the others.
+    const int q = warp & 3, hh = (warp - F::SOFTMAX_AT / 32) >> 2, half = lane >> 4;
+    const int tid = threadIdx.x - F::SOFTMAX_AT;
     const int row = 32 * q + 16 * hh + (lane & 15);
     const uint32_t lanes = static_cast<uint32_t>(32 * q + 16 * hh) << 16;
-    uint32_t* nan_map = reinterpret_cast<uint32_t*>(smem + F::NAN_AT);
-    int* lim_s = reinterpret_cast<int*>(smem + F::LIM_AT);
-    float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
+    const int sub0 = 4 * half;  // this lane's groups of 16 keys
     const uint32_t q_base = smem_u32(smem) + F::Q_AT;
     Cursor cc = start;
     bool begins = true;
-    int pv = 0, start_gi = 0;
-    int limit = -1, lim_all = 0, lim_any = -1;
-    float qf = 0.f, m = -INFINITY, l = 0.f, vref = 1.f, vtop = 0.f;
+    int start_gi = 0;
+    uint32_t t = 0;        // the slot whose turn it is,
+    RowState cur, other;   // its row and the other slot's
+    cur.jobs = cur.prods = other.jobs = other.prods = 0;
+    auto turn = [&]() {
+      const RowState x = cur;
+      cur = other;
+      other = x;
+      t ^= 1;
+    };
 
     // The tile's queries as operand rows, and its rows' limits.
-    auto begin_tile = [&]() {
+    auto begin_tile = [&](int n) {
       const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
       bool bad;
       const Item it = item_of(P, cc.b, bad);
       const int rows = P.n_q * P.share;
-      {
-        constexpr int TPR = 2;     // threads per row
-        constexpr int PPT = 8 / TPR;          // 16-element pieces per thread
-        const int r = tid / TPR, part = tid % TPR;
-        const int rr = rt * F::ROWS + r, i = rr / P.share;
+#pragma unroll 1
+      for (int r = tid / 2; r < P.tile_rows; r += NST / 2) {
+        const int part = tid & 1;  // a panel of 64 columns
+        const int rr = rt * P.tile_rows + r, i = rr / P.share;
         const bool in = rr < rows && i < it.fresh;
         const int head = kv * P.share + (rr - i * P.share);
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(P.Q) +
                                    (((long long)cc.b * P.h + head) * P.n_q + i) * P.d_h;
-        uint4 raw[PPT][2];
+        uint4 raw[8];
         float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < PPT; ++k) {
-          const int col = (part * PPT + k) * 16;
+        for (int k = 0; k < 8; ++k) {
+          const int col = part * 64 + k * 8;
+          raw[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (in && col < P.d_h) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + col));
+          const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            raw[k][e] = make_uint4(0u, 0u, 0u, 0u);
-            if (in && col < P.d_h) raw[k][e] = __ldg(reinterpret_cast<const uint4*>(src + col) + e);
-            const uint32_t x[4] = {raw[k][e].x, raw[k][e].y, raw[k][e].z, raw[k][e].w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[f] << 16)),
-                                     fabsf(__uint_as_float(x[f] & 0xffff0000u))));
-          }
+          for (int f = 0; f < 4; ++f)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[f] << 16)),
+                                   fabsf(__uint_as_float(x[f] & 0xffff0000u))));
         }
-#pragma unroll
-        for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^(7 - E) for a largest element in [2^E, 2^(E + 1))
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        // times 2^(14 - E) for a largest element in [2^E, 2^(E + 1))
         int E = (int)(__float_as_uint(top) >> 23) - 127;
-        E = E > 127 || top == 0.f ? 7 : max(E, -100);
-        const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+        E = E > 127 || top == 0.f ? 14 : max(E, -100);
+        const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
 #pragma unroll
-        for (int k = 0; k < PPT; ++k) {
-          uint32_t hi[4], lo[4];
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          uint32_t o[4];
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const uint4 u = raw[k][f / 2];
-            const uint32_t x0 = f % 2 ? u.z : u.x, x1 = f % 2 ? u.w : u.y;
-            split4<0>(__uint_as_float(x0 << 16) * up, __uint_as_float(x0 & 0xffff0000u) * up,
-                                 __uint_as_float(x1 << 16) * up, __uint_as_float(x1 & 0xffff0000u) * up,
-                                 hi[f], lo[f]);
-          }
-          const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          const int c = part * PPT + k;
-          sts128(q_base + swz(r, c), h4);
-          sts128(q_base + F::OPERAND + swz(r, c), l4);
+          for (int f = 0; f < 4; ++f)
+            o[f] = pack_half(__uint_as_float(x[f] << 16) * up, __uint_as_float(x[f] & 0xffff0000u) * up);
+          sts128(q_base + (r / F::ROWS) * F::OPERAND + part * F::PANEL + swz(r % F::ROWS, k),
+                 make_uint4(o[0], o[1], o[2], o[3]));
         }
         if (part == 0) {
-          qf_s[r] = P.cl2 * __uint_as_float((uint32_t)(E - 7 + 127) << 23);
+          qf_s[r] = P.cl2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
           lim_s[r] = !in ? -1 : P.causal_tail ? max(-1, it.total - it.fresh + i) : it.total - 1;
         }
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      named_sync(1, NST);
-      for (int e = tid; e < F::ROWS * 4; e += NST) nan_map[e] = 0u;  // the last tile's was read
-      named_sync(1, NST);
-      qf = qf_s[row];
-      limit = lim_s[row];
-      // the limits of the tile's first and last row that see a key
-      const int i0 = rt * F::ROWS / P.share;
-      const int i1 = min((min(rows, (rt + 1) * F::ROWS) - 1) / P.share, it.fresh - 1);
-      const int back = it.total - it.fresh;
-      lim_any = i1 < i0 ? -1 : P.causal_tail ? back + i1 : it.total - 1;
-      lim_all = P.causal_tail ? max(0, back + i0) : it.total - 1;
-      m = -INFINITY;
-      l = 0.f;
-      vref = 1.f;
-      vtop = 0.f;
-      start_gi = cc.gi;
-    };
-
-    // z of this warp's rows times f (f may differ from row to row).
-    auto scale_z = [&](float f) {
-      tc_fence_after();
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint32_t at = tmem + lanes + F::Z_COL + p * 128u;
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          uint32_t o[32];
-          tmem_ld_x2_32<64>(at + 32 * cb, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tmem_st_x2_32<64>(at + 32 * cb, o);
-        }
+      if (lane == 0) {  // for the slots that have a group of this tile
+        const int left = min(cc.ng - cc.gi, steps - n);
+        if (pair || left > 1 || t == 0) mbar_arrive(q_full);
+        if (pair || left > 1 || t == 1) mbar_arrive(q_full + 1);
       }
-      tmem_wait_st();
+      named_sync(1, NST);
+      for (int e = tid; e < 2 * F::ROWS * 4; e += NST) nan_map[e] = 0u;  // the last tile's was read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tile_full);
+      named_sync(1, NST);
+      cur.qf = qf_s[row];
+      cur.limit = lim_s[row];
+      other.qf = qf_s[pair ? row + F::ROWS : row];
+      other.limit = lim_s[pair ? row + F::ROWS : row];
+      cur.m = other.m = -INFINITY;
+      cur.l = other.l = 0.f;
+      cur.vref = other.vref = 1.f;
+      cur.vtop = other.vtop = 0.f;
+      cur.fresh = other.fresh = true;
+      start_gi = cc.gi;
     };
 
 #pragma unroll 1
     for (int n = 0; n < steps; ++n) {
-      const int stage = n % F::STAGES, b = n & 1;
       const bool ends = cc.gi == cc.ng - 1 || n == steps - 1;
-      if (begins) begin_tile();
-      cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
-      cache_wait(s_full + b, (n >> 1) & 1, ctl);
-      __syncwarp();
-      {
+      if (begins) begin_tile(n);
+      const Meta* meta = metas + n % F::METAS;
+      const int kb = cc.gi * KEYS;
+      cache_wait(meta_full + n % F::METAS, (n / F::METAS) & 1, ctl);
+#pragma unroll 1
+      for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
+        cache_wait(s_full + t, cur.jobs & 1, ctl);
+        ++cur.jobs;
+        __syncwarp();
         tc_fence_after();
-        const Meta* meta = metas + stage;
-        const int kb = cc.gi * KEYS;
+        const uint32_t s_at = tmem + lanes + F::S_COL + t * 128;
         const uint32_t found = meta->found;
-        const bool masked = kb + KEYS - 1 > lim_all || found != 0xffu;
-        float s[F::SUBS][16];
-        {
-          const uint32_t at = tmem + lanes + F::S_COL + b * KEYS;
-          uint32_t x[64];
-          tmem_ld_x2_64<64>(at, x);
-          tmem_wait_ld();
+        const bool masked =
+            __any_sync(0xffffffffu, cur.limit >= 0 && kb + KEYS - 1 > cur.limit) || found != 0xffu;
+        uint32_t x[64];
+        tmem_ld_x2_64<64>(s_at, x);
+        tmem_wait_ld();
+        auto two = [&](int k) { return make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
+        // scores s = f x, with a factor for every 16 keys
+        float f[4], mx = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 64; ++k) s[k / 16][k % 16] = __uint_as_float(x[k]);
-        }
-        const int sub0 = 4 * half;  // this lane's groups of 16 keys
-        float mx = -INFINITY;
+        for (int i = 0; i < 4; ++i) f[i] = cur.qf * meta->ks[sub0 + i];
+        if (!masked && !__any_sync(0xffffffffu, fminf(fminf(f[0], f[1]), fminf(f[2], f[3])) < 0.f)) {
 #pragma unroll
-        for (int i = 0; i < F::SUBS; ++i) {
-          const float f = qf * meta->ks[sub0 + i];
-          const int seen = found >> (sub0 + i) & 1 ? limit - kb - 16 * (sub0 + i) : -1;
+          for (int i = 0; i < 4; ++i) {
+            float y = fmaxf(two(16 * i).x, two(16 * i).y);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            s[i][k] *= f;
-            if (masked && k > seen) s[i][k] = -INFINITY;
-            mx = fmaxf(mx, s[i][k]);
+            for (int k = 16 * i + 2; k < 16 * i + 16; k += 2) y = max3(y, two(k).x, two(k).y);
+            mx = fmaxf(mx, f[i] * y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int seen = found >> (sub0 + i) & 1 ? cur.limit - kb - 16 * (sub0 + i) : -1;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float y = k > seen ? -INFINITY : __uint_as_float(x[16 * i + k]) * f[i];
+              x[16 * i + k] = __float_as_uint(y);
+              mx = fmaxf(mx, y);
+            }
+            f[i] = 1.f;
           }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        // a row's reference is raised only where a weight would pass 2^1.75
+        // a row's reference is raised only where a weight would pass 2^8
         float alpha = 1.f;
-        if (mx > m + RAISE) {
-          alpha = ex2_approx(m - mx);
-          m = mx;
-          l *= alpha;
+        if (mx > cur.m + MANY_RAISE) {
+          alpha = ex2_approx(cur.m - mx);
+          cur.m = mx;
+          cur.l *= alpha;
         }
-        const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < F::SUBS; ++i) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            s[i][k] = ex2_approx(s[i][k] - base);
-            l += s[i][k];
-          }
-        }
-        if (masked && tid < KEYS)
-          mend_values(smem_u32(smem) + stage * STAGE + SIDE, tid,
-                      (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, F::ROWS, lim_s, nan_map);
-        // Weights, times 2^7 vs / vref with vs / vref in [2^-4, 1]. vref
-        // follows vs, a smaller one down to 2^-60 of the largest only, so
-        // that z cannot overflow. Blocks further apart go one after another.
-        uint32_t todo = meta->single ? 0u : found;
-        bool fresh = begins;  // z holds nothing yet
-        bool again = false;   // a further round
-        const uint32_t p_at = tmem + lanes + F::S_COL + b * KEYS;
-#pragma unroll 1
-        do {
-          float top = meta->top;
-          uint32_t take = found;
-          if (todo) {
-            take = take_of(meta, todo, top);
-            todo &= ~take;
-          }
-          const float seen = vtop;
-          vtop = fmaxf(vtop, top);
-          float by = 1.f;
-          if (top > 0.f && (top > vref || top < 0.25f * vref)) {
-            const float to = fmaxf(top, vtop * 8.6736173798840355e-19f);  // 2^-60
-            if (seen > 0.f) by = vref / to;
-            vref = to;
-          }
-          // z may be changed, and weights of this group replaced, only behind
-          // the products so far (all but the last one are: the scores of this
-          // group came after them)
-          const float f = alpha * by;
-          const bool scales = !fresh && __any_sync(0xffffffffu, f != 1.f);
-          if (scales || again) {
-            cache_wait(p_free, (pv - 1) & 1, ctl);
-            __syncwarp();
-            if (scales) scale_z(f);
-          }
+        const float base = cur.m == -INFINITY ? 0.f : cur.m;
+        // Weights are held times 2^7 vs / vref with vs / vref in [2^-4, 1].
+        // vref follows vs, a smaller one down to 2^-60 of the largest only, so
+        // that z cannot overflow. follow: what z is to be multiplied with
+        // before products with scales up to top are added to it.
+        auto follow = [&](float top) {
+          const float seen = cur.vtop;
+          cur.vtop = fmaxf(cur.vtop, top);
+          float by = alpha;
           alpha = 1.f;
-          fresh = false;
-          again = true;
-          uint32_t hi[4 * F::SUBS], lo[4 * F::SUBS];
-#pragma unroll
-          for (int i = 0; i < F::SUBS; ++i) {
-            const float r = take >> (sub0 + i) & 1 ? UNIT * (meta->vs[sub0 + i] / vref) : 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              split4<4>(s[i][4 * k] * r, s[i][4 * k + 1] * r, s[i][4 * k + 2] * r, s[i][4 * k + 3] * r,
-                        hi[4 * i + k], lo[4 * i + k]);
+          if (top > 0.f && (top > cur.vref || top < 0.25f * cur.vref)) {
+            const float to = fmaxf(top, cur.vtop * 8.6736173798840355e-19f);  // 2^-60
+            if (seen > 0.f) by *= cur.vref / to;
+            cur.vref = to;
           }
-          tmem_st_x2_16<16>(p_at, hi);
-          tmem_st_x2_16<16>(p_at + 32, lo);
+          return by;
+        };
+        const bool single = meta->single;  // else blocks go one after another
+        float by = 1.f, r[4] = {UNIT, UNIT, UNIT, UNIT};
+        if (single) {
+          by = follow(meta->top);
+          const float u = UNIT / cur.vref;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = found >> (sub0 + i) & 1 ? u * meta->vs[sub0 + i] : 0.f;
+        }
+        uint32_t w[32];
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          float2 p = __ffma2_rn(two(k), make_float2(f[k / 16], f[k / 16]), make_float2(-base, -base));
+          p = make_float2(ex2_approx(p.x), ex2_approx(p.y));
+          sum[k / 2 % 2] = __fadd2_rn(sum[k / 2 % 2], p);
+          p = __fmul2_rn(p, make_float2(r[k / 16], r[k / 16]));
+          w[k / 2] = pack_half(p.x, p.y);
+        }
+        cur.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // z times by. (The slot's earlier value products are done: its scores
+        // came after them.)
+        auto scale_z = [&](float by) {
+          if (cur.fresh || !__any_sync(0xffffffffu, by != 1.f)) return;
+#pragma unroll 1
+          for (int cb = 0; cb < 2; ++cb) {
+            uint32_t o[32];
+            const uint32_t at = tmem + lanes + F::Z_COL + t * 128 + 32 * cb;
+            tmem_ld_x2_32<64>(at, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+            tmem_st_x2_32<64>(at, o);
+          }
+        };
+        auto give = [&](const uint32_t (&w)[32]) {
+          tmem_st_x2_32<32>(s_at, w);
           tmem_wait_st();
-          if (masked) fence_async_shared();  // value rows may have been mended
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + b);  // a warp may be a group ahead of another
-          ++pv;
-        } while (todo);
+          if (lane == 0) mbar_arrive(p_full + t);
+          ++cur.prods;
+          cur.fresh = false;
+        };
+        if (single) {
+          scale_z(by);
+          give(w);
+        } else {
+          // A round for the blocks whose scales are near one another. (Those
+          // weights are rounded a second time.)
+          uint32_t todo = found;
+          bool again = false;
+#pragma unroll 1
+          do {
+            float top = meta->top;
+            uint32_t take = found;
+            if (todo) take = take_of(meta, todo, top);
+            todo &= ~take;
+            by = follow(top);
+            if (again) {
+              cache_wait(z_full + t, (cur.prods - 1) & 1, ctl);
+              __syncwarp();
+              tc_fence_after();
+            }
+            scale_z(by);
+            again = true;
+            const float u = 1.f / cur.vref;
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float g = take >> (sub0 + i) & 1 ? u * meta->vs[sub0 + i] : 0.f;
+#pragma unroll
+              for (int k = 8 * i; k < 8 * i + 8; ++k) {
+                const float2 p = __half22float2(reinterpret_cast<const __half2&>(w[k]));
+                v[k] = g == 0.f ? 0u : pack_half(p.x * g, p.y * g);
+              }
+            }
+            give(v);
+          } while (todo);
+        }
       }
       if (ends) {
         // ---- the summary of the keys [start_gi, cc.gi] of the tile ----
-        // (one phase after the other: the parity tells two apart, not three)
-        if (pv > 1) cache_wait(p_free, (pv - 2) & 1, ctl);
-        cache_wait(p_free, (pv - 1) & 1, ctl);
+        if (!cur.fresh) cache_wait(z_full + t, (cur.prods - 1) & 1, ctl);
+        if (!other.fresh) cache_wait(z_full + (t ^ 1), (other.prods - 1) & 1, ctl);
         __syncwarp();
         tc_fence_after();
         const bool whole = start_gi == 0 && cc.gi == cc.ng - 1;
         const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
-        const long long slot = 2ll * blockIdx.x + (start_gi == 0 ? 1 : 0);
+        const long long at = 2ll * blockIdx.x + (start_gi == 0 ? 1 : 0);
         float* const pz = P.part + 4ll * P.ranges * P.slot_rows;
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const bool none = limit < 0 || l == 0.f;
-        // columns [c, c + 16) of row r: v = z sum, to Z or to the workspace
-        auto store = [&](int r, int c, const float (&v)[16], float scale) {
-          const int rr = rt * F::ROWS + r;
-          if (rr >= P.n_q * P.share || c >= P.d_vh) return;
-          const int i = rr / P.share, head = kv * P.share + (rr - i * P.share);
-          const uint32_t bad = nan_map[r * 4 + (c >> 5)] >> (c & 31);
-          float o[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = bad >> k & 1 ? __int_as_float(0x7fffffff) : v[k] * scale;
-          if (whole) {
-            uint4* z = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.Z) +
-                                                ((long long)cc.b * P.n_q + i) * P.h * P.d_vh +
-                                                (long long)head * P.d_vh + c);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              z[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-          } else {
-            float4* z = reinterpret_cast<float4*>(pz + (slot * P.slot_rows + r) * P.d_vh + c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              z[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+#pragma unroll 1
+        for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
+          // the row's m and l, and what a slot's z is multiplied with
+          float m = cur.m, l = cur.l, wa = cur.vref, wb = 0.f;
+          if (!pair) {
+            m = fmaxf(cur.m, other.m);
+            const float ea = cur.m == m ? 1.f : ex2_approx(cur.m - m);
+            const float eb = other.m == m ? 1.f : ex2_approx(other.m - m);
+            l = cur.l * ea + other.l * eb;
+            wa *= ea;
+            wb = other.vref * eb;
           }
-        };
-        const float scale = none ? 0.f : (1.f / UNIT) * (whole ? 1.f / l : 1.f);
-        if (!whole && half == 0 && rt * F::ROWS + row < P.n_q * P.share) {
-          P.part[2 * (slot * P.slot_rows + row)] = none ? -INFINITY : m;
-          P.part[2 * (slot * P.slot_rows + row) + 1] = none ? 0.f : l;
-        }
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const bool none = cur.limit < 0 || l == 0.f;
+          const float scale = (1.f / UNIT) * (whole ? 1.f / l : 1.f);
+          const int r = row + (pair ? t * F::ROWS : 0), rr = rt * P.tile_rows + r;
+          const int i = rr / P.share, head = kv * P.share + (rr - i * P.share);
+          const bool stored = rr < P.n_q * P.share;
+          if (stored && !whole && half == 0) {
+            P.part[2 * (at * P.slot_rows + r)] = none ? -INFINITY : m;
+            P.part[2 * (at * P.slot_rows + r) + 1] = none ? 0.f : l;
+          }
+#pragma unroll 1
+          for (int cb = 0; cb < 2; ++cb) {
+            float v[32];
+            {
+              uint32_t x[32];
+              tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + t * 128 + 32 * cb, x);
+              tmem_wait_ld();
 #pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          uint32_t x[32], y[32];
-          tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + 32 * cb, x);
-          tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + 128 + 32 * cb, y);
-          tmem_wait_ld();
+              for (int k = 0; k < 32; ++k) v[k] = cur.fresh ? 0.f : __uint_as_float(x[k]) * wa;
+            }
+            if (!pair) {
+              uint32_t x[32];
+              tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + (t ^ 1) * 128 + 32 * cb, x);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            float v[16];
+              for (int k = 0; k < 32; ++k)
+                if (!other.fresh) v[k] = fmaf(__uint_as_float(x[k]), wb, v[k]);
+            }
+            const int c0 = 64 * half + 32 * cb;
+            const uint32_t bad = nan_map[r * 4 + (c0 >> 5)];
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[k] = none ? 0.f : fmaf(__uint_as_float(y[c + k]), 0.0625f, __uint_as_float(x[c + k])) * vref;
-            store(row, 64 * half + 32 * cb + c, v, scale);
+            for (int k = 0; k < 32; ++k) {
+              v[k] = none ? 0.f : v[k] * scale;
+              if (bad >> k & 1) v[k] = __int_as_float(0x7fffffff);
+            }
+            if (!stored) continue;
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {  // d_vh is a multiple of 16
+              if (c0 + c >= P.d_vh) continue;
+              if (whole) {
+                uint4* z = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.Z) +
+                                                    ((long long)cc.b * P.n_q + i) * P.h * P.d_vh +
+                                                    (long long)head * P.d_vh + c0 + c);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float* o = v + c + 8 * k;
+                  z[k] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                    pack_bf16x2(o[6], o[7]));
+                }
+              } else {
+                float4* z = reinterpret_cast<float4*>(pz + (at * P.slot_rows + r) * P.d_vh + c0 + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  z[k] = make_float4(v[c + 4 * k], v[c + 4 * k + 1], v[c + 4 * k + 2], v[c + 4 * k + 3]);
+              }
+            }
           }
         }
         tc_fence_before();
@@ -1408,9 +1571,9 @@ mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s) {
   while (P.bt % box) box /= 2;
   if (!make_cache_maps(P, box, ROW)) return MHA_ERR_CUDA;
   P.ranges = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
-  P.tile_cost = P.tile_rows == Many::ROWS ? 3 : 2 + P.slot_rows / 4;
+  P.tile_cost = P.tile_rows > 16 ? 3 : 2 + P.slot_rows / 4;
   cudaError_t e;
-  if (P.tile_rows == Many::ROWS)
+  if (P.tile_rows > 16)
     e = launch(cache_attention_many_kernel, Many::THREADS, Many::SMEM, P, s);
   else if (P.slot_rows == 1)
     e = launch(cache_attention_few_kernel<1>, Few::THREADS, Few::SMEM, P, s);
