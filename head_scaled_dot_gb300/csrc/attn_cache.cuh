@@ -180,24 +180,29 @@ __device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
-// The bounded wait with everything but the first look out of line: a kernel
-// whose warps have different roles waits in many places, and its code has to
-// stay in the instruction cache (with the whole wait in each place, the
-// tensor-core kernels were 80 to 170 KB long and stalled on fetching it). Once
-// any wait of the CTA has given up, all others return at once.
-static __device__ __noinline__ bool cache_wait_slow(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
-  if (*w.abort) return false;
-  return mbar_wait_slow(bar, parity, w);
-}
+// The bounded wait, kept short: a kernel whose warps have different roles waits
+// in many places, and its code has to stay in the instruction cache. (Not out
+// of line: a call keeps the caller's values in local memory, which shared
+// memory has taken the cache of.) Once any wait of the CTA has given up, all
+// others return at once.
 __device__ __forceinline__ bool cache_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
   if (mbar_try_wait(bar, parity)) return true;
-  return cache_wait_slow(bar, parity, w);
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  for (uint32_t it = 1; it != 0; ++it) {
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+    if (*w.abort) return false;
+    if (globaltimer_ns() - t0 > w.limit_ns) break;
+  }
+  report_error(w, MHA_ERR_DEVICE_TIMEOUT);
+  return false;
 }
 
 // Waits, with a limit of its own, until a barrier phase has completed although
 // a wait has been given up: for copies or products still in flight.
-static __device__ __noinline__ void wait_in_flight(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void wait_in_flight(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
   for (uint32_t it = 1; it != 0; ++it) {
     if (mbar_try_wait_sleep(bar, parity, 20000)) return;
     if (globaltimer_ns() - t0 > 100000000ull) return;

@@ -155,6 +155,15 @@ __device__ __forceinline__ void tmem_st_x2_16(uint32_t taddr, const uint32_t (&r
       "r"(r[14]), "r"(r[15])
       : "memory");
 }
+template <int OFF>
+__device__ __forceinline__ void tmem_ld_x2_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15}, [%16], %17;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "n"(OFF));
+}
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -221,11 +230,14 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // Groups of 16 keys whose values go into the next product: those of `todo`
 // within 2^2 of its largest scale `top` (and those without a positive scale,
 // so that every round takes at least one).
-static __device__ __noinline__ uint32_t take_of(const Meta* m, uint32_t todo, float& top) {
-  top = 0.f;
+__device__ __forceinline__ float top_of(const Meta* m, uint32_t todo) {
+  float top = 0.f;
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
     if (todo >> i & 1) top = fmaxf(top, m->vs[i]);
+  return top;
+}
+__device__ __forceinline__ uint32_t take_of(const Meta* m, uint32_t todo, float top) {
   uint32_t take = 0;
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
@@ -233,11 +245,28 @@ static __device__ __noinline__ uint32_t take_of(const Meta* m, uint32_t todo, fl
   return take;
 }
 
+// The largest scale of the next product of a group, whose groups of 16 keys are
+// taken out of `todo` (0 from the start: one product for all).
+__device__ __forceinline__ float next_top(const Meta* m, uint32_t& todo) {
+  if (!todo) return m->top;
+  const float top = top_of(m, todo);
+  todo &= ~take_of(m, todo, top);
+  return top;
+}
+
 // Value row `row` of the stage at `src`, which not every query row sees: its
 // NaN bytes are zeroed, so that weights of 0 stay without effect, and noted for
 // the rows that do see the key at position `key`.
-static __device__ __noinline__ void mend_values(uint32_t src, int row, bool seen, int key, int rows,
+__device__ __forceinline__ void mend_values(uint32_t src, int row, bool seen, int key, int rows,
                                                 const int* lim, uint32_t* nan_map) {
+  uint32_t found = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 u = lds128(src + swz(row, c));
+    found |= ((u.x & 0x7f7f7f7fu) + 0x01010101u) | ((u.y & 0x7f7f7f7fu) + 0x01010101u) |
+             ((u.z & 0x7f7f7f7fu) + 0x01010101u) | ((u.w & 0x7f7f7f7fu) + 0x01010101u);
+  }
+  if (!(found & 0x80808080u)) return;
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     const uint32_t at = src + swz(row, c);
@@ -546,10 +575,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         const uint64_t pd = p_desc + b * (KEYS * 32 >> 4);
         const uint32_t at = tmem + F::Z_COL + b * 32;
         do {
-          if (todo) {
-            float top;
-            todo &= ~take_of(m, todo, top);
-          }
+          if (todo) todo &= ~take_of(m, todo, top_of(m, todo));
           ok = ok && cache_wait(p_full + b, pv & 1, ctl);
           if (!ok) break;
           tc_fence_after();
@@ -783,6 +809,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
           float top = meta->top;
           uint32_t take = 0xffu;
           if (todo) {
+            top = top_of(meta, todo);
             take = take_of(meta, todo, top);
             todo &= ~take;
           }
@@ -931,7 +958,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 // ---------------------------------------------------------------------------
 
 struct Many {
-  static constexpr int CONVERT_WARPS = 4, SOFTMAX_WARPS = 8;
+  static constexpr int CONVERT_WARPS = 4;
+  static constexpr int SOFTMAX_WARPS = 8;
   static constexpr int CONVERT_AT = 128, SOFTMAX_AT = CONVERT_AT + 32 * CONVERT_WARPS;  // first threads
   static constexpr int THREADS = SOFTMAX_AT + 32 * SOFTMAX_WARPS;
   static constexpr int STAGES = 2;
@@ -976,27 +1004,43 @@ struct TileLimits {
   }
 };
 
+// The values' scales over a tile: its z is held over vref. vref follows the
+// scales, a smaller one down to 2^-60 of the largest only, so that z cannot
+// overflow, and stays within [1, 4) times the largest of a product. (The
+// threads that convert and those of the softmax each follow it for themselves.)
+struct Follow {
+  float vref = 1.f, vtop = 0.f;
+  // What z is to be multiplied with before products with scales up to top.
+  __device__ __forceinline__ float operator()(float top) {
+    const float seen = vtop, was = vref;
+    vtop = fmaxf(vtop, top);
+    if (!(top > 0.f && (top > vref || top < 0.25f * vref))) return 1.f;
+    vref = fmaxf(top, vtop * 8.6736173798840355e-19f);  // 2^-60
+    return seen > 0.f ? was / vref : 1.f;
+  }
+};
+
 // What a softmax thread keeps of a query row, per slot.
 struct RowState {
-  float qf, m, l, vref, vtop;
+  float qf, m, l;  // l: times UNIT, as the weights
+  float owed;      // what z is still to be multiplied with
   int limit;       // keys up to here are seen
   uint32_t jobs;   // score tiles so far
   uint32_t prods;  // value products so far
   bool fresh;      // no key of this tile yet: z holds nothing
 };
 
-// Half a tile (8 pieces of 16 bytes a thread) of e4m3 numbers from a stage as
-// fp16 into registers, and from there into the operand. A quarter of a warp
-// takes rows r and r + 4 and half their columns, and one of the two rows stores
-// its 16-byte pieces in the other order: no two of its lanes meet on a bank,
-// neither reading nor writing.
-__device__ __forceinline__ void read_piece(uint32_t src, int i, int row, int col, bool odd, uint4& a, uint4& b) {
-  const int r = row + 8 * (i >> 1), c = col + 4 * (i & 1);
-  const uint4 u = lds128(src + swz(r, c));
-  const uint32_t x0 = odd ? u.z : u.x, x1 = odd ? u.w : u.y, y0 = odd ? u.x : u.z, y1 = odd ? u.y : u.w;
-  a = make_uint4(e4m3_lo(x0), e4m3_hi(x0), e4m3_lo(x1), e4m3_hi(x1));
-  b = make_uint4(e4m3_lo(y0), e4m3_hi(y0), e4m3_lo(y1), e4m3_hi(y1));
-}
+// Piece i (of 8) of a thread's share of a tile: 16 e4m3 numbers from a stage,
+// as fp16. A quarter of a warp takes two neighbouring rows, of one half its
+// columns in this panel, of the other in the other one: no two of its lanes
+// meet on a bank, neither reading nor writing.
+struct Piece {
+  int row, panel, col;  // col: of four groups of 16 in the panel
+  __device__ __forceinline__ Piece(int warp, int lane, int i)
+      : row(32 * warp + 2 * (lane >> 3) + (lane >> 2 & 1) + 8 * (i >> 1)),
+        panel((i & 1) ^ (lane >> 2 & 1)),
+        col(lane & 3) {}
+};
 
 __global__ void __launch_bounds__(Many::THREADS, 1)
     cache_attention_many_kernel(const __grid_constant__ CacheAttnParams P) {
@@ -1097,13 +1141,13 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       const uint32_t idesc_z = idesc_f16_f32(128, P.d_vh, 0, 1);
       const int panels = P.d_h > 64 ? 2 : 1;
       const uint32_t base = smem_u32(smem);
-      const uint64_t q_desc = sdesc_sw128(base + F::Q_AT + t * F::OPERAND, 16, 1024);
+      const uint64_t q_desc = sdesc_sw128(base + F::Q_AT + (pair ? t * F::OPERAND : 0), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(base + F::KEY_AT, 16, 1024);
       const uint64_t v_desc = sdesc_sw128(base + F::VALUE_AT, F::PANEL, 1024);
       const uint32_t s_tmem = tmem + F::S_COL + t * 128, z_tmem = tmem + F::Z_COL + t * 128;
       Cursor cc = start;
       bool ok = true, fresh = true;
-      uint32_t tile = 0, pv = 0;
+      uint32_t tile = 0, pv = 0, rounds[2] = {0, 0};
       for (int n = 0; n < steps; ++n) {
         if (pair || (n & 1) == t) {
           const uint32_t par = (n >> 1) & 1;
@@ -1126,14 +1170,11 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           }
           umma_commit(s_full + t);
           umma_commit(k_free + (n & 1));
-          ok = cache_wait(v_full + (n & 1), par, ctl);
           const Meta* m = metas + n % F::METAS;
           uint32_t todo = m->single ? 0u : m->found;
           do {
-            if (todo) {
-              float top;
-              todo &= ~take_of(m, todo, top);
-            }
+            if (todo) todo &= ~take_of(m, todo, top_of(m, todo));
+            ok = ok && cache_wait(v_full + (n & 1), (n & 1 ? rounds[1]++ : rounds[0]++) & 1, ctl);
             ok = ok && cache_wait(p_full + t, pv++ & 1, ctl);
             if (!ok) break;
             tc_fence_after();
@@ -1141,10 +1182,10 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
             for (int k = 0; k < KEYS / 16; ++k)
               umma_ts(z_tmem, s_tmem + k * 8, v_desc + (uint64_t)(k * 16 * ROW >> 4), idesc_z, !fresh || k > 0);
             umma_commit(z_full + t);
+            umma_commit(v_free + (n & 1));
             fresh = false;
           } while (todo);
           if (!ok) break;
-          umma_commit(v_free + (n & 1));
         }
         if (advance(cc, first, P.B, unit)) fresh = true;
       }
@@ -1156,13 +1197,12 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
     // (After a wait that gave up the work goes on without waiting: nothing
     // else here can block.)
     const int tid = threadIdx.x - F::CONVERT_AT;
-    const int row = tid / 32 * 32 + (lane >> 3) + (lane & 4), col = lane & 3;
-    const bool odd = (lane & 4) != 0;
     const uint32_t base = smem_u32(smem);
     Cursor cc = start;
     bool begins = true, waited = false;
-    uint32_t tile = 0, mends = 0;
-    int lim_all = 0, lim_any = -1;
+    uint32_t tile = 0, mends = 0, rounds[2] = {0, 0};  // of even and odd groups' values
+    int lim_all = 0, lim_any = -1, before = -1;        // (of which the last one was)
+    Follow follow;
     for (int n = 0; n < steps; ++n) {
       const int stage = n % F::STAGES;
       const uint32_t last = (n - 1) & 1, last_par = ((n - 1) >> 1) & 1;
@@ -1172,68 +1212,108 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         const TileLimits lim(P, item_of(P, cc.b, bad), cc.pr % P.tiles);
         lim_all = lim.lim_all;
         lim_any = lim.lim_any;
+        follow = Follow();
         waited = false;
       }
       cache_wait(full + stage, (n / F::STAGES) & 1, ctl);
       cache_wait(meta_full + n % F::METAS, (n / F::METAS) & 1, ctl);
       __syncwarp();
       const int kb = cc.gi * KEYS;
-      const uint32_t found = metas[n % F::METAS].found;
+      const Meta* meta = metas + n % F::METAS;
+      const uint32_t found = meta->found;
       const bool masked = kb + KEYS - 1 > lim_all || found != 0xffu;
       if ((masked || ends) && !waited) {  // (each of the barrier's phases is met)
         cache_wait(tile_full, tile++ & 1, ctl);
         waited = true;
         __syncwarp();
       }
-#pragma unroll 1
-      for (int side = 0; side < 2; ++side) {
-        const uint32_t src = base + stage * STAGE + side * SIDE;
-        if (side && masked) {
-          mend_values(src, tid, (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, P.tile_rows, lim_s,
-                      nan_map);
-          fence_async_shared();  // the next bytes come by TMA
-          __syncwarp();
-          if (lane == 0) mbar_arrive(mended);
-          cache_wait(mended, mends++ & 1, ctl);
-          __syncwarp();
-        }
-        uint4 a[8], b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) read_piece(src, i, row, col, odd, a[i], b[i]);
-        __syncwarp();
-        if (side && lane == 0) mbar_arrive(empty + stage);
-        if (n > 0) cache_wait((side ? v_free : k_free) + last, last_par, ctl);
-        __syncwarp();
-        const uint32_t dst = base + (side ? F::VALUE_AT : F::KEY_AT);
+      const uint32_t src = base + stage * STAGE;
+      uint4 u[8];
+      auto read = [&](uint32_t src) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = row + 8 * (i >> 1);
-          const uint32_t to = dst + (i & 1) * F::PANEL;
-          sts128(to + swz(r, 2 * col + (odd ? 1 : 0)), a[i]);
-          sts128(to + swz(r, 2 * col + (odd ? 0 : 1)), b[i]);
+          const Piece p(warp & 3, lane, i);
+          u[i] = lds128(src + swz(p.row, 4 * p.panel + p.col));
+        }
+        __syncwarp();
+      };
+      // times g[0] for the first 16 of the warp's 32 rows, g[1] for the others
+      auto write = [&](uint32_t dst, const __half2 (&g)[2]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const Piece p(warp & 3, lane, i);
+          const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            o[k] = k & 1 ? e4m3_hi(x[k / 2]) : e4m3_lo(x[k / 2]);
+            const __half2 v = __hmul2(reinterpret_cast<const __half2&>(o[k]), g[i / 4]);
+            o[k] = reinterpret_cast<const uint32_t&>(v);
+          }
+          const uint32_t to = dst + p.panel * F::PANEL;
+          sts128(to + swz(p.row, 2 * p.col), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(to + swz(p.row, 2 * p.col + 1), make_uint4(o[4], o[5], o[6], o[7]));
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive((side ? v_full : k_full) + (n & 1));
+      };
+      read(src);
+      if (n > 0) cache_wait(k_free + last, last_par, ctl);  // the operand's last readers
+      __syncwarp();
+      const __half2 one = __float2half2_rn(1.f);
+      write(base + F::KEY_AT, {one, one});
+      if (lane == 0) mbar_arrive(k_full + (n & 1));
+
+      if (masked) {
+        mend_values(src + SIDE, tid, (found >> (tid >> 4) & 1) && kb + tid <= lim_any, kb + tid, P.tile_rows, lim_s,
+                    nan_map);
+        fence_async_shared();  // the next bytes come by TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mended);
+        cache_wait(mended, mends++ & 1, ctl);
+        __syncwarp();
       }
+      read(src + SIDE);
+      if (lane == 0) mbar_arrive(empty + stage);
+      // Values over vref; blocks whose scales are too far apart go one after
+      // another, so that every product's are within [2^-4, 1] times e4m3: exact
+      // for powers of two, else rounded to 11 bits.
+      uint32_t todo = meta->single ? 0u : found;
+#pragma unroll 1
+      do {
+        const uint32_t all = todo;
+        follow(next_top(meta, todo));
+        const uint32_t take = all ? all & ~todo : found;
+        __half2 g[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int sub = 2 * (warp & 3) + i;
+          g[i] = __float2half2_rn(take >> sub & 1 ? meta->vs[sub] / follow.vref : 0.f);
+        }
+        if (before >= 0) cache_wait(v_free + before, ((before ? rounds[1] : rounds[0]) - 1) & 1, ctl);
+        __syncwarp();
+        write(base + F::VALUE_AT, g);
+        if (lane == 0) mbar_arrive(v_full + (n & 1));
+        before = n & 1;
+        if (before) ++rounds[1]; else ++rounds[0];
+      } while (todo);
       begins = ends;
       advance(cc, first, P.B, unit);
     }
   } else {
     // ---- softmax ----
-    // A warp has 16 rows of each slot: lane i < 16 holds the first 64 keys of
-    // row i, lane i + 16 the others.
-    const int q = warp & 3, hh = (warp - F::SOFTMAX_AT / 32) >> 2, half = lane >> 4;
-    const int tid = threadIdx.x - F::SOFTMAX_AT;
-    const int row = 32 * q + 16 * hh + (lane & 15);
-    const uint32_t lanes = static_cast<uint32_t>(32 * q + 16 * hh) << 16;
-    const int sub0 = 4 * half;  // this lane's groups of 16 keys
+    // A warp has 16 rows of each slot, and takes the slots in turn: one slot's
+    // products run while the other one's weights are computed. Lane i < 16
+    // holds the first 64 keys of row i, lane i + 16 the others.
+    const int tid = threadIdx.x - F::SOFTMAX_AT, half = lane >> 4;
+    const int row16 = 32 * (warp & 3) + 16 * (warp >> 2 & 1), row = row16 + (lane & 15);
+    const uint32_t lanes = static_cast<uint32_t>(row16) << 16;
     const uint32_t q_base = smem_u32(smem) + F::Q_AT;
     Cursor cc = start;
-    bool begins = true;
     int start_gi = 0;
-    uint32_t t = 0;        // the slot whose turn it is,
-    RowState cur, other;   // its row and the other slot's
+    Follow follow;
+    uint32_t t = 0;       // the slot whose turn it is,
+    RowState cur, other;  // its row and the other slot's
     cur.jobs = cur.prods = other.jobs = other.prods = 0;
     auto turn = [&]() {
       const RowState x = cur;
@@ -1248,9 +1328,9 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       bool bad;
       const Item it = item_of(P, cc.b, bad);
       const int rows = P.n_q * P.share;
+      const int part = tid & 1;  // a panel of 64 columns
 #pragma unroll 1
-      for (int r = tid / 2; r < P.tile_rows; r += NST / 2) {
-        const int part = tid & 1;  // a panel of 64 columns
+      for (int r = tid / 2; r < P.tile_rows; r += F::ROWS) {
         const int rr = rt * P.tile_rows + r, i = rr / P.share;
         const bool in = rr < rows && i < it.fresh;
         const int head = kv * P.share + (rr - i * P.share);
@@ -1263,11 +1343,13 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           const int col = part * 64 + k * 8;
           raw[k] = make_uint4(0u, 0u, 0u, 0u);
           if (in && col < P.d_h) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + col));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
           const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[f] << 16)),
-                                   fabsf(__uint_as_float(x[f] & 0xffff0000u))));
+          for (int e = 0; e < 4; ++e)
+            top = max3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         // times 2^(14 - E) for a largest element in [2^E, 2^(E + 1))
@@ -1279,8 +1361,8 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
           uint32_t o[4];
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            o[f] = pack_half(__uint_as_float(x[f] << 16) * up, __uint_as_float(x[f] & 0xffff0000u) * up);
+          for (int e = 0; e < 4; ++e)
+            o[e] = pack_half(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
           sts128(q_base + (r / F::ROWS) * F::OPERAND + part * F::PANEL + swz(r % F::ROWS, k),
                  make_uint4(o[0], o[1], o[2], o[3]));
         }
@@ -1293,8 +1375,8 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       __syncwarp();
       if (lane == 0) {  // for the slots that have a group of this tile
         const int left = min(cc.ng - cc.gi, steps - n);
-        if (pair || left > 1 || t == 0) mbar_arrive(q_full);
-        if (pair || left > 1 || t == 1) mbar_arrive(q_full + 1);
+        if (pair || left > 1 || (n & 1) == 0) mbar_arrive(q_full);
+        if (pair || left > 1 || (n & 1) == 1) mbar_arrive(q_full + 1);
       }
       named_sync(1, NST);
       for (int e = tid; e < 2 * F::ROWS * 4; e += NST) nan_map[e] = 0u;  // the last tile's was read
@@ -1307,165 +1389,140 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       other.limit = lim_s[pair ? row + F::ROWS : row];
       cur.m = other.m = -INFINITY;
       cur.l = other.l = 0.f;
-      cur.vref = other.vref = 1.f;
-      cur.vtop = other.vtop = 0.f;
+      cur.owed = other.owed = 1.f;
       cur.fresh = other.fresh = true;
+      follow = Follow();
       start_gi = cc.gi;
     };
 
+    // The slot's weights are there: z times `by`, then the value product.
+    auto give = [&](float by) {
+      if (!cur.fresh && __any_sync(0xffffffffu, by != 1.f)) {
 #pragma unroll 1
-    for (int n = 0; n < steps; ++n) {
-      const bool ends = cc.gi == cc.ng - 1 || n == steps - 1;
-      if (begins) begin_tile(n);
-      const Meta* meta = metas + n % F::METAS;
-      const int kb = cc.gi * KEYS;
-      cache_wait(meta_full + n % F::METAS, (n / F::METAS) & 1, ctl);
-#pragma unroll 1
-      for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
-        cache_wait(s_full + t, cur.jobs & 1, ctl);
-        ++cur.jobs;
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t s_at = tmem + lanes + F::S_COL + t * 128;
-        const uint32_t found = meta->found;
-        const bool masked =
-            __any_sync(0xffffffffu, cur.limit >= 0 && kb + KEYS - 1 > cur.limit) || found != 0xffu;
-        uint32_t x[64];
-        tmem_ld_x2_64<64>(s_at, x);
-        tmem_wait_ld();
-        auto two = [&](int k) { return make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
-        // scores s = f x, with a factor for every 16 keys
-        float f[4], mx = -INFINITY;
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t o[16];
+          const uint32_t at = tmem + lanes + F::Z_COL + t * 128 + 16 * cb;
+          tmem_ld_x2_16<64>(at, o);
+          tmem_wait_ld_r(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = cur.qf * meta->ks[sub0 + i];
-        if (!masked && !__any_sync(0xffffffffu, fminf(fminf(f[0], f[1]), fminf(f[2], f[3])) < 0.f)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = fmaxf(two(16 * i).x, two(16 * i).y);
-#pragma unroll
-            for (int k = 16 * i + 2; k < 16 * i + 16; k += 2) y = max3(y, two(k).x, two(k).y);
-            mx = fmaxf(mx, f[i] * y);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int seen = found >> (sub0 + i) & 1 ? cur.limit - kb - 16 * (sub0 + i) : -1;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float y = k > seen ? -INFINITY : __uint_as_float(x[16 * i + k]) * f[i];
-              x[16 * i + k] = __float_as_uint(y);
-              mx = fmaxf(mx, y);
-            }
-            f[i] = 1.f;
-          }
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        // a row's reference is raised only where a weight would pass 2^8
-        float alpha = 1.f;
-        if (mx > cur.m + MANY_RAISE) {
-          alpha = ex2_approx(cur.m - mx);
-          cur.m = mx;
-          cur.l *= alpha;
-        }
-        const float base = cur.m == -INFINITY ? 0.f : cur.m;
-        // Weights are held times 2^7 vs / vref with vs / vref in [2^-4, 1].
-        // vref follows vs, a smaller one down to 2^-60 of the largest only, so
-        // that z cannot overflow. follow: what z is to be multiplied with
-        // before products with scales up to top are added to it.
-        auto follow = [&](float top) {
-          const float seen = cur.vtop;
-          cur.vtop = fmaxf(cur.vtop, top);
-          float by = alpha;
-          alpha = 1.f;
-          if (top > 0.f && (top > cur.vref || top < 0.25f * cur.vref)) {
-            const float to = fmaxf(top, cur.vtop * 8.6736173798840355e-19f);  // 2^-60
-            if (seen > 0.f) by *= cur.vref / to;
-            cur.vref = to;
-          }
-          return by;
-        };
-        const bool single = meta->single;  // else blocks go one after another
-        float by = 1.f, r[4] = {UNIT, UNIT, UNIT, UNIT};
-        if (single) {
-          by = follow(meta->top);
-          const float u = UNIT / cur.vref;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = found >> (sub0 + i) & 1 ? u * meta->vs[sub0 + i] : 0.f;
-        }
-        uint32_t w[32];
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          float2 p = __ffma2_rn(two(k), make_float2(f[k / 16], f[k / 16]), make_float2(-base, -base));
-          p = make_float2(ex2_approx(p.x), ex2_approx(p.y));
-          sum[k / 2 % 2] = __fadd2_rn(sum[k / 2 % 2], p);
-          p = __fmul2_rn(p, make_float2(r[k / 16], r[k / 16]));
-          w[k / 2] = pack_half(p.x, p.y);
-        }
-        cur.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        // z times by. (The slot's earlier value products are done: its scores
-        // came after them.)
-        auto scale_z = [&](float by) {
-          if (cur.fresh || !__any_sync(0xffffffffu, by != 1.f)) return;
-#pragma unroll 1
-          for (int cb = 0; cb < 2; ++cb) {
-            uint32_t o[32];
-            const uint32_t at = tmem + lanes + F::Z_COL + t * 128 + 32 * cb;
-            tmem_ld_x2_32<64>(at, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-            tmem_st_x2_32<64>(at, o);
-          }
-        };
-        auto give = [&](const uint32_t (&w)[32]) {
-          tmem_st_x2_32<32>(s_at, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + t);
-          ++cur.prods;
-          cur.fresh = false;
-        };
-        if (single) {
-          scale_z(by);
-          give(w);
-        } else {
-          // A round for the blocks whose scales are near one another. (Those
-          // weights are rounded a second time.)
-          uint32_t todo = found;
-          bool again = false;
-#pragma unroll 1
-          do {
-            float top = meta->top;
-            uint32_t take = found;
-            if (todo) take = take_of(meta, todo, top);
-            todo &= ~take;
-            by = follow(top);
-            if (again) {
-              cache_wait(z_full + t, (cur.prods - 1) & 1, ctl);
-              __syncwarp();
-              tc_fence_after();
-            }
-            scale_z(by);
-            again = true;
-            const float u = 1.f / cur.vref;
-            uint32_t v[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float g = take >> (sub0 + i) & 1 ? u * meta->vs[sub0 + i] : 0.f;
-#pragma unroll
-              for (int k = 8 * i; k < 8 * i + 8; ++k) {
-                const float2 p = __half22float2(reinterpret_cast<const __half2&>(w[k]));
-                v[k] = g == 0.f ? 0u : pack_half(p.x * g, p.y * g);
-              }
-            }
-            give(v);
-          } while (todo);
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+          tmem_st_x2_16<64>(at, o);
         }
       }
-      if (ends) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + t);
+      ++cur.prods;
+      cur.fresh = false;
+    };
+
+#pragma unroll 1
+    for (int n = 0; n < steps;) {
+      begin_tile(n);
+      const int count = min(cc.ng - cc.gi, steps - n), last = n + count;
+#pragma unroll 1
+      for (int kb = cc.gi * KEYS; n < last; ++n, kb += KEYS) {
+        const Meta* meta = metas + n % F::METAS;
+        cache_wait(meta_full + n % F::METAS, (n / F::METAS) & 1, ctl);
+        uint32_t todo = meta->single ? 0u : meta->found;
+        const float to = follow(next_top(meta, todo));
+#pragma unroll 1
+        for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
+          cache_wait(s_full + t, cur.jobs & 1, ctl);
+          ++cur.jobs;
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t s_at = tmem + lanes + F::S_COL + t * 128;
+          const uint32_t found = meta->found;
+          uint32_t x[64];
+          tmem_ld_x2_64<64>(s_at, x);
+          float ks[4], least = 1.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ks[i] = cur.qf * meta->ks[4 * half + i];
+            least = fminf(least, ks[i]);
+          }
+          // scores: x times ks, or (with masks, or a negative scale) x
+          const bool plain = found == 0xffu &&
+                             !__any_sync(0xffffffffu, (cur.limit >= 0 && kb + KEYS - 1 > cur.limit) || least < 0.f);
+          tmem_wait_ld();
+          auto two = [&](int k) { return make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
+          float mx = -INFINITY;
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y = fmaxf(two(16 * i).x, two(16 * i).y);
+#pragma unroll
+              for (int k = 16 * i + 2; k < 16 * i + 16; k += 2) y = max3(y, two(k).x, two(k).y);
+              mx = fmaxf(mx, ks[i] * y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int sub = 4 * half + i;
+              const int seen = found >> sub & 1 ? cur.limit - kb - 16 * sub : -1;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float y = k > seen ? -INFINITY : __uint_as_float(x[16 * i + k]) * ks[i];
+                x[16 * i + k] = __float_as_uint(y);
+                mx = fmaxf(mx, y);
+              }
+              ks[i] = 1.f;
+            }
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          // a row's reference is raised only where a weight would pass 2^8
+          float alpha = cur.owed;
+          cur.owed = 1.f;
+          if (mx > cur.m + MANY_RAISE) {
+            const float a = ex2_approx(cur.m - mx);
+            cur.m = mx;
+            cur.l *= a;
+            alpha *= a;
+          }
+          const float e0 = 7.f - (cur.m == -INFINITY ? 0.f : cur.m);
+          static_assert(UNIT == 128.f, "2^7");
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = h; k < h + 32; k += 2) {
+              const float2 e = __ffma2_rn(two(k), make_float2(ks[k / 16], ks[k / 16]), make_float2(e0, e0));
+              const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              sum[k / 2 % 2] = __fadd2_rn(sum[k / 2 % 2], p);
+              w[(k - h) / 2] = pack_half(p.x, p.y);
+            }
+            tmem_st_x2_16<32>(s_at + h / 2, w);
+          }
+          cur.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          give(alpha * to);  // (the slot's earlier value products are done: its scores came after them)
+        }
+        if (!pair) cur.owed *= to;  // the other slot's z follows later
+        // Further rounds, for blocks whose scales are too far apart for one
+        // product: round by round, as one conversion of the values serves both
+        // slots.
+        while (todo) {
+          const float by = follow(next_top(meta, todo));
+          if (!pair) {
+            cur.owed *= by;
+            turn();
+          }
+#pragma unroll 1
+          for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
+            cache_wait(z_full + t, (cur.prods - 1) & 1, ctl);
+            __syncwarp();
+            tc_fence_after();
+            give(by);
+          }
+        }
+      }
+      cc.gi += count - 1;
+      {
         // ---- the summary of the keys [start_gi, cc.gi] of the tile ----
+        // z goes through the queries' place in shared memory, so that whole
+        // rows of it are written.
         if (!cur.fresh) cache_wait(z_full + t, (cur.prods - 1) & 1, ctl);
         if (!other.fresh) cache_wait(z_full + (t ^ 1), (other.prods - 1) & 1, ctl);
         __syncwarp();
@@ -1474,80 +1531,78 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         const int kv = cc.pr / P.tiles, rt = cc.pr - kv * P.tiles;
         const long long at = 2ll * blockIdx.x + (start_gi == 0 ? 1 : 0);
         float* const pz = P.part + 4ll * P.ranges * P.slot_rows;
+        const uint32_t stage = q_base + (warp - F::SOFTMAX_AT / 32) * (16 * ROW);
 #pragma unroll 1
-        for (int slot = pair ? 0 : 1; slot < 2; ++slot, turn()) {
-          // the row's m and l, and what a slot's z is multiplied with
-          float m = cur.m, l = cur.l, wa = cur.vref, wb = 0.f;
+        for (int slot = pair ? 0 : 1; slot < 2; ++slot) {
+          // a pair's slots have a tile each; else both have a sum of the one tile
+          float m = cur.m, l = cur.l;
+          float wa = cur.fresh ? 0.f : follow.vref * cur.owed, wb = 0.f;  // what the slots' z are multiplied with
           if (!pair) {
             m = fmaxf(cur.m, other.m);
             const float ea = cur.m == m ? 1.f : ex2_approx(cur.m - m);
             const float eb = other.m == m ? 1.f : ex2_approx(other.m - m);
             l = cur.l * ea + other.l * eb;
-            wa *= ea;
-            wb = other.vref * eb;
+            // (a NaN stays, however small its weight)
+            if (!cur.fresh) wa = fmaxf(wa * ea, 1.2e-38f);
+            if (!other.fresh) wb = fmaxf(follow.vref * other.owed * eb, 1.2e-38f);
           }
           l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const int row0 = pair ? t * F::ROWS : 0;
           const bool none = cur.limit < 0 || l == 0.f;
-          const float scale = (1.f / UNIT) * (whole ? 1.f / l : 1.f);
-          const int r = row + (pair ? t * F::ROWS : 0), rr = rt * P.tile_rows + r;
-          const int i = rr / P.share, head = kv * P.share + (rr - i * P.share);
-          const bool stored = rr < P.n_q * P.share;
-          if (stored && !whole && half == 0) {
-            P.part[2 * (at * P.slot_rows + r)] = none ? -INFINITY : m;
-            P.part[2 * (at * P.slot_rows + r) + 1] = none ? 0.f : l;
+          const float scale = whole ? 1.f / l : 1.f / UNIT;
+          if (!whole && half == 0 && rt * P.tile_rows + row0 + row < P.n_q * P.share) {
+            P.part[2 * (at * P.slot_rows + row0 + row)] = none ? -INFINITY : m;
+            P.part[2 * (at * P.slot_rows + row0 + row) + 1] = none ? 0.f : l * (1.f / UNIT);
           }
 #pragma unroll 1
-          for (int cb = 0; cb < 2; ++cb) {
-            float v[32];
-            {
-              uint32_t x[32];
-              tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + t * 128 + 32 * cb, x);
-              tmem_wait_ld();
+          for (int cb = 0; cb < 4; ++cb) {
+            // columns [16 cb, 16 cb + 16) of this half row's 64
+            const uint32_t z_at = tmem + lanes + F::Z_COL + 16 * cb;
+            uint32_t v[16];
+            tmem_ld_x2_16<64>(z_at + t * 128, v);
+            tmem_wait_ld_r(v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = cur.fresh ? 0.f : __uint_as_float(x[k]) * wa;
-            }
+            for (int k = 0; k < 16; ++k) v[k] = wa == 0.f ? 0u : __float_as_uint(__uint_as_float(v[k]) * wa);
             if (!pair) {
-              uint32_t x[32];
-              tmem_ld_x2_32<64>(tmem + lanes + F::Z_COL + (t ^ 1) * 128 + 32 * cb, x);
-              tmem_wait_ld();
+              uint32_t y[16];
+              tmem_ld_x2_16<64>(z_at + (t ^ 1) * 128, y);
+              tmem_wait_ld_r(y);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!other.fresh) v[k] = fmaf(__uint_as_float(x[k]), wb, v[k]);
+              for (int k = 0; k < 16; ++k)
+                if (wb != 0.f) v[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), wb, __uint_as_float(v[k])));
             }
-            const int c0 = 64 * half + 32 * cb;
-            const uint32_t bad = nan_map[r * 4 + (c0 >> 5)];
+            const uint32_t bad = nan_map[(row0 + row) * 4 + 2 * half + (cb >> 1)] >> (16 * (cb & 1));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              v[k] = none ? 0.f : v[k] * scale;
-              if (bad >> k & 1) v[k] = __int_as_float(0x7fffffff);
+            for (int k = 0; k < 16; ++k)
+              v[k] = bad >> k & 1 ? 0x7fffffffu : none ? 0u : __float_as_uint(__uint_as_float(v[k]) * scale);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(stage + swz(lane & 15, half * 4 + k),
+                     make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+            __syncwarp();
+            const int chunk = lane & 7, col = 64 * (chunk >> 2) + 16 * cb + 4 * (chunk & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rho = 4 * k + (lane >> 3), r = row0 + row16 + rho;
+              const int rr = rt * P.tile_rows + r, i = rr / P.share, head = kv * P.share + (rr - i * P.share);
+              const uint4 o = lds128(stage + swz(rho, chunk));
+              if (rr >= P.n_q * P.share || col >= P.d_vh) continue;
+              if (whole)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(P.Z) +
+                                          (((long long)cc.b * P.n_q + i) * P.h + head) * P.d_vh + col) =
+                    make_uint2(pack_bf16x2(__uint_as_float(o.x), __uint_as_float(o.y)),
+                               pack_bf16x2(__uint_as_float(o.z), __uint_as_float(o.w)));
+              else
+                *reinterpret_cast<uint4*>(pz + (at * P.slot_rows + r) * P.d_vh + col) = o;
             }
-            if (!stored) continue;
-#pragma unroll
-            for (int c = 0; c < 32; c += 16) {  // d_vh is a multiple of 16
-              if (c0 + c >= P.d_vh) continue;
-              if (whole) {
-                uint4* z = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.Z) +
-                                                    ((long long)cc.b * P.n_q + i) * P.h * P.d_vh +
-                                                    (long long)head * P.d_vh + c0 + c);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float* o = v + c + 8 * k;
-                  z[k] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                    pack_bf16x2(o[6], o[7]));
-                }
-              } else {
-                float4* z = reinterpret_cast<float4*>(pz + (at * P.slot_rows + r) * P.d_vh + c0 + c);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  z[k] = make_float4(v[c + 4 * k], v[c + 4 * k + 1], v[c + 4 * k + 2], v[c + 4 * k + 3]);
-              }
-            }
+            __syncwarp();
           }
+          if (pair) turn();
         }
+        named_sync(1, NST);  // before the next tile's queries come
         tc_fence_before();
       }
-      begins = ends;
-      advance(cc, first, P.B, unit);
+      if (n < steps) advance(cc, first, P.B, unit);
     }
   }
   tc_fence_before();

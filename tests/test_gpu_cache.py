@@ -445,6 +445,10 @@ ATTEND = [
     ([20, 3], [20, 5], 20, 2, 1, 64, 64, 16, "bf16", True),        # all rows new; more than total
     ([3000], [150], 150, 2, 1, 64, 64, 128, "bf16", True),
     ([100] * 70, None, 1, 2, 1, 32, 32, 16, "bf16", True),
+    ([12000, 700], [17, 20], 20, 4, 4, 128, 128, 64, "bf16", True),  # some groups of keys per CTA
+    ([5000, 700], [70, 64], 70, 16, 4, 128, 112, 32, "bf16", True),
+    ([900, 2500], [64, 1], 64, 2, 1, 64, 48, 16, "bf16", True),      # one tile of rows exactly
+    ([900, 2500], None, 129, 1, 1, 80, 128, 16, "bf16", False),      # one row past it
 ]
 
 
@@ -474,6 +478,47 @@ def test_attention_with_scales_of_every_size(dtype):
     cache.t["Ks"].copy_(torch.exp2(-e - 4).expand(30, 2))
     cache.sync()
     attend_and_check(cache, [450, 3], None, 2, 2, 64, 64, dtype, True, 22)
+
+
+@pytest.mark.parametrize("n_q", [2, 20, 150])
+def test_attention_of_many_keys_with_scales_of_every_size(n_q):
+    """As above with many groups of keys, and with zero and negative scales."""
+    cache = Cache(200, 2, 16, 64, 64, 23, spread=0)
+    e = torch.arange(200, device="cuda").float()[:, None] % 7
+    cache.t["Vs"].copy_(torch.exp2(e * 10 - 30).expand(200, 2))
+    cache.t["Ks"].copy_(torch.exp2(-e - 4).expand(200, 2))
+    cache.sync()
+    attend_and_check(cache, [2900, 150], None, n_q, 2, 64, 64, "bf16", True, 24)
+    cache.t["Vs"][::5] = 0
+    cache.t["Ks"][1::5] *= -1
+    cache.t["Ks"][2::5] = 0
+    cache.sync()
+    attend_and_check(cache, [2900, 150], None, n_q, 2, 64, 64, "bf16", True, 24)
+
+
+@pytest.mark.parametrize("n_q", [20, 150])
+def test_nan_and_stale_rows_with_many_rows(n_q):
+    bt, d, h = 16, 64, 2
+    total = [n_q + 203]
+    cache = Cache(30, h, bt, d, d, 33)
+    table = table_of(total, bt, 30, 24, 5, fill=1 << 30)
+    at = lambda p: (int(table[0, p // bt]), slice(None), p % bt)
+    for p in range(total[0], -(-total[0] // bt) * bt):  # past the end
+        cache.t["K"][at(p)] = 0x7f
+        cache.t["V"][at(p)] = 0xff
+    cache.sync()
+    Q, clean = attend_and_check(cache, total, None, n_q, h, d, d, "bf16", True, 34, table)
+    args = (ints(table.tolist()), ints(total), d ** -0.5)
+    # rows are positions 203 on: row 9 is the first that sees the value, 12 the key
+    cache.t["V"][at(212)][..., 5] = 0xff
+    Z = mha.attention_cache(Q, *cache.args, *args, causal_tail=True)
+    assert torch.equal(Z[:, :9], clean[:, :9])
+    nan = torch.isnan(Z[:, 9:]).reshape(1, n_q - 9, h, d)
+    assert nan[..., 5].all() and not nan[..., :5].any() and not nan[..., 6:].any()
+    cache.t["K"][at(215)] = 0x7f
+    Z = mha.attention_cache(Q, *cache.args, *args, causal_tail=True)
+    assert torch.equal(Z[:, :9], clean[:, :9])
+    assert torch.isnan(Z[:, 12:]).all() and not torch.isnan(Z[:, 9:12, :5]).any()
 
 
 def test_stale_rows_and_nan_do_not_reach_rows_that_do_not_see_them():
@@ -544,7 +589,7 @@ def test_attention_is_the_same_whatever_the_workspace_holds():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
-@pytest.mark.parametrize("n_q,share", [(1, 1), (4, 4), (200, 4)])
+@pytest.mark.parametrize("n_q,share", [(1, 1), (4, 4), (200, 4), (20, 4)])
 def test_calls_in_a_row_end_and_agree(n_q, share):
     """Many groups per CTA, call after call without a wait between them: no
     wait inside the kernel runs out, and every call gives the same bits."""
