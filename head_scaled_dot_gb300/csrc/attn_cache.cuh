@@ -44,7 +44,7 @@ struct CacheAttnParams {
 // Merges the summaries of the tiles that more than one range had a part of,
 // and writes the rows that see no key (attn_cache.cu).
 cudaError_t launch_cache_merge(const CacheAttnParams& P, mha_dtype dt, cudaStream_t s);
-// Tensor-core kernel for bf16 queries and head sizes up to 128 (attn_cache_tc.cu).
+// Tensor-core kernels for bf16 queries and head sizes up to 128 (attn_cache_tc.cu).
 mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s);
 // The tensor maps of the cache, for boxes of `box` rows of `width` bytes.
 bool make_cache_maps(CacheAttnParams& P, int box, int width);

@@ -1,43 +1,45 @@
 // attn_cache_tc.cu - attention over the 8-bit cache on the fifth-generation
 // tensor cores: bf16 queries, head sizes up to 128.
 //
-// The bytes of the cache go from HBM to the tensor cores as they are: TMA puts
-// tiles of 128 keys into shared memory, and both products are tcgen05.mma of
-// kind f8f6f4 with the key and value tiles as e4m3 operands and fp32 sums in
-// tensor memory. What is multiplied with them is written as a sum of two e4m3
-// numbers, x = hi + lo / 16:
-//   queries  a row is scaled by a power of two to a largest element in
-//            [2^7, 2^8). bf16's 8 bits are exactly the 4 of hi and the 4 of
-//            lo, down to 2^-13 of the row's largest element.
-//   weights  p = 2^{s - m}, times 2^7 vs / vref: 8 bits, down to 2^-17 of the
-//            weight of the row's reference m.
-//
 // Two kernels, by the query rows that share a key/value head (new rows times
-// query heads per key/value head):
-//   few, up to 16: the keys are the MMA's 128 rows and the queries its
-//     columns, hi of up to 16 rows and lo of them: S^T = K Q^T, z^T = V^T P^T
-//     with N = 32. A thread holds one key's scores of all rows, so the work
-//     follows the number of rows; a row's maximum lies across the threads, but
-//     is only needed when a weight would pass the reference, which one barrier
-//     with an OR finds out. Two groups of four warps take the groups of keys
-//     in turn, each with a summary of its own.
-//   many: 128 rows a tile, one per lane: S = Q K^T, z = P V. hi and lo of the
-//     queries go into the same accumulator (lo is not scaled there: exact down
-//     to 2^-9 of the row's largest element, off by at most 2^-17 of it below),
-//     those of the weights into two.
+// query heads per key/value head). Both are persistent, one CTA per SM over its
+// range of the list of groups of 128 keys; TMA puts the bytes of a group's keys
+// and values into a ring in shared memory (warps 0 and 2), warps 1 and 3 issue
+// the products, whose sums stay in tensor memory, and the softmax warps turn
+// scores into weights. z stays in tensor memory too; it is rescaled only where
+// a row's reference is raised or the values' scale moves.
 //
-// Pipeline of a CTA (one per SM, persistent over its range of the list of
-// groups): warps 0, 2 and 3 fill the ring of stages, warp 1 issues the
-// products (the scores of the next group before the value product of the
-// current one), the softmax warps turn scores into weights. z stays in tensor
-// memory; it is rescaled only where a row's reference is raised or the values'
-// scale moves.
+//   few, up to 16 rows, bound by HBM: the bytes are the operands of tcgen05.mma
+//     of kind f8f6f4. The keys are its 128 rows and the queries its columns:
+//     S^T = K Q^T, z^T = V^T P^T. What is multiplied with the cache's numbers
+//     is written as the sum of two e4m3 numbers, x = hi + lo / 16, hi of up to
+//     16 rows and lo of them, N = 32:
+//       queries  a row is scaled by a power of two to a largest element in
+//                [2^7, 2^8). bf16's 8 bits are exactly the 4 of hi and the 4 of
+//                lo, down to 2^-13 of the row's largest element.
+//       weights  p = 2^{s - m}, times 2^7 vs / vref: 8 bits, down to 2^-17 of
+//                the weight of the row's reference m.
+//     A thread holds one key's scores of all rows, so the work follows the
+//     number of rows; a row's maximum lies across the threads, but is only
+//     needed when a weight would pass the reference, which one barrier with an
+//     OR finds out. Two groups of four warps take the groups of keys in turn,
+//     each with a summary of its own. (As 128 rows of an MMA of 128 x 128 x 32,
+//     most of them empty, the queries cost 123 cycles a product, 1000 of the
+//     1490 that HBM needs for a group.)
+//   many: four warps turn a group's bytes into fp16 once, for up to 256 rows:
+//     two slots of 128 rows, S = Q K^T and z = P V of kind f16, a slot's
+//     products running while the other one's weights are computed. e4m3 is a
+//     subset of fp16 and bf16's 8 bits, scaled by a power of two per row, fit in
+//     its 11. (With the bytes as operands and hi and lo of queries and weights
+//     the products were twice as many, each as long as one in fp16, and the
+//     weights cost two conversions more: 145 us against 92 for 2 x 4 key/value
+//     heads of 2048 rows over 6000 keys, d = 128. Rows of up to 128 take as
+//     long either way.) With at most 128 rows the slots take the groups of keys
+//     in turn and their sums are added at the end.
 //
-// Measured against the mma.sync kernel of attn_cache.cu, which this one
-// replaced for these types: its m16n8k16 products alone took 512 cycles per 32
-// keys and SM on the profiler, more than HBM's share of 370. With few rows as
-// the 128 operand rows (a row in each of four groups of 32 lanes) an MMA of
-// 128 x 128 x 32 took 123 cycles, 1000 of the 1490 that HBM needs for a group.
+// Against the mma.sync kernel of attn_cache.cu, which these replaced for bf16:
+// its m16n8k16 products alone took 512 cycles per 32 keys and SM, more than
+// HBM's share of 370.
 #include "attn_cache.cuh"
 
 namespace mha {
@@ -47,9 +49,9 @@ constexpr int KEYS = 128;               // keys per group
 constexpr int ROW = 128;                // bytes of a row in shared memory
 constexpr int SIDE = KEYS * ROW;        // one side of a stage
 constexpr int STAGE = 2 * SIDE;
-constexpr float RAISE = 1.75f;          // a weight is at most 2^1.75 ...
+constexpr float RAISE = 1.75f;          // few rows: a weight is at most 2^1.75 ...
 constexpr float UNIT = 128.f;           // ... times this: e4m3's largest is 448 > 2^8.75
-constexpr float MANY_RAISE = 8.f;       // many rows: fp16 weights, at most 2^8 times UNIT
+constexpr float MANY_RAISE = 8.f;       // many rows: at most 2^8 times UNIT, of fp16's 2^16
 constexpr float HEADROOM = 1.f;         // few rows: references are set above the scores seen
 constexpr float NOTHING = -3e38f;       // a row's reference before its first key; finite, so that
                                         // a masked score's distance from it is -inf too
@@ -198,9 +200,8 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool v) {
   return r != 0;
 }
 
-// Four values x (at most 448) as hi and lo of x = hi + lo / 2^SHIFT, four
-// e4m3 numbers each. fp16 in between holds 11 bits.
-template <int SHIFT>
+// Four values x (at most 448) as hi and lo of x = hi + lo / 16, four e4m3
+// numbers each. fp16 in between holds 11 bits.
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi,
                                        uint32_t& lo) {
   const uint32_t h0 = pack_half(a, b), h1 = pack_half(c, d);
@@ -211,7 +212,7 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
       : "=r"(e)
       : "r"(h0), "r"(h1));
   hi = e;
-  const __half2 k = __float2half2_rn((float)(1 << SHIFT));
+  const __half2 k = __float2half2_rn(16.f);
   const uint32_t g0 = e4m3_lo(e), g1 = e4m3_hi(e);
   const __half2 r0 = __hmul2(__hsub2(reinterpret_cast<const __half2&>(h0), reinterpret_cast<const __half2&>(g0)), k);
   const __half2 r1 = __hmul2(__hsub2(reinterpret_cast<const __half2&>(h1), reinterpret_cast<const __half2&>(g1)), k);
@@ -292,9 +293,11 @@ __device__ __forceinline__ void mend_values(uint32_t src, int row, bool seen, in
   }
 }
 
-// Warp 0 fills the ring with the key tiles of the groups from lc on, warp 2 with the value tiles and the scales, each walking the groups for itself. A
-// stage is full after an arrival of each for its tiles, one for the scales, and
-// the tiles' bytes.
+// Warp 0 fills the ring of NS stages with the key tiles of the groups from lc
+// on, warp 2 with the value tiles, and NM places with the scales; each walks
+// the groups for itself. A stage is full after an arrival of each for its tiles
+// and the tiles' bytes; there_meta gets one for the scales (with NM = NS it is
+// the stage's barrier too).
 template <int NS, int NM>
 __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first,
                                           const int* totals, int unit, Cursor lc, int steps,
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        split4<4>(__uint_as_float(x[2 * k] << 16) * up, __uint_as_float(x[2 * k] & 0xffff0000u) * up,
+        split4(__uint_as_float(x[2 * k] << 16) * up, __uint_as_float(x[2 * k] & 0xffff0000u) * up,
                   __uint_as_float(x[2 * k + 1] << 16) * up, __uint_as_float(x[2 * k + 1] & 0xffff0000u) * up,
                   hi[k], lo[k]);
       const uint32_t q_base = smem_u32(smem) + F::Q_AT;
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
           uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int r = 0; r < NR; r += 4)
-            split4<4>(s[r] * f, r + 1 < NR ? s[r + 1 < NR ? r + 1 : r] * f : 0.f,
+            split4(s[r] * f, r + 1 < NR ? s[r + 1 < NR ? r + 1 : r] * f : 0.f,
                       r + 2 < NR ? s[r + 2 < NR ? r + 2 : r] * f : 0.f,
                       r + 3 < NR ? s[r + 3 < NR ? r + 3 : r] * f : 0.f, hi[r / 4], lo[r / 4]);
           sts128(p_at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
@@ -955,6 +958,18 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // Many rows: S = Q K^T, z = P V
+//
+// What bounds it: 92 us for 2 sequences x 4 key/value heads x 2048 query rows
+// (512 new ones of 4 heads each) over 6000 keys, d = 128, 496 TFLOP/s; the
+// products alone are 24 us. A group of keys for a pair of slots takes about
+// 4600 cycles, 3400 of them the eight softmax warps (for 128 rows 650 for the
+// loads and maxima and 950 for the weights, on its own 930 together; products
+// and conversions left out, nothing changes). Beginning a tile takes 6 us (its
+// queries, first keys) and ending it 6 (128 KB of sums that another CTA has the
+// rest of), merging 8. Sixteen softmax warps, eight a slot, took 106 us (at 80
+// registers each values went to local memory, which is L2 as shared memory has
+// taken the cache), four a slot with a row per thread 107 (the slots fall into
+// step and the tensor cores idle) and 112 to 121 with an order between them.
 // ---------------------------------------------------------------------------
 
 struct Many {
@@ -1143,7 +1158,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       const uint32_t base = smem_u32(smem);
       const uint64_t q_desc = sdesc_sw128(base + F::Q_AT + (pair ? t * F::OPERAND : 0), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(base + F::KEY_AT, 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(base + F::VALUE_AT, F::PANEL, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + (pair || t == 0 ? F::VALUE_AT : F::Q_AT + F::OPERAND), F::PANEL, 1024);
       const uint32_t s_tmem = tmem + F::S_COL + t * 128, z_tmem = tmem + F::Z_COL + t * 128;
       Cursor cc = start;
       bool ok = true, fresh = true;
@@ -1201,7 +1216,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
     Cursor cc = start;
     bool begins = true, waited = false;
     uint32_t tile = 0, mends = 0, rounds[2] = {0, 0};  // of even and odd groups' values
-    int lim_all = 0, lim_any = -1, before = -1;        // (of which the last one was)
+    int lim_all = 0, lim_any = -1, before = 0;         // (of which the last one was)
     Follow follow;
     for (int n = 0; n < steps; ++n) {
       const int stage = n % F::STAGES;
@@ -1290,11 +1305,15 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           const int sub = 2 * (warp & 3) + i;
           g[i] = __float2half2_rn(take >> sub & 1 ? meta->vs[sub] / follow.vref : 0.f);
         }
-        if (before >= 0) cache_wait(v_free + before, ((before ? rounds[1] : rounds[0]) - 1) & 1, ctl);
+        // The operand's last readers: with one tile of queries the second
+        // one's place holds the values of odd groups.
+        const int held = pair ? before : n & 1;
+        const uint32_t times = held ? rounds[1] : rounds[0];
+        if (times > 0) cache_wait(v_free + held, (times - 1) & 1, ctl);
         __syncwarp();
-        write(base + F::VALUE_AT, g);
-        if (lane == 0) mbar_arrive(v_full + (n & 1));
+        write(base + (pair || (n & 1) == 0 ? F::VALUE_AT : F::Q_AT + F::OPERAND), g);
         before = n & 1;
+        if (lane == 0) mbar_arrive(v_full + before);
         if (before) ++rounds[1]; else ++rounds[0];
       } while (todo);
       begins = ends;
@@ -1554,6 +1573,15 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
             P.part[2 * (at * P.slot_rows + row0 + row)] = none ? -INFINITY : m;
             P.part[2 * (at * P.slot_rows + row0 + row) + 1] = none ? 0.f : l * (1.f / UNIT);
           }
+          // A store instruction has four rows: lane's are 4 k + lane / 8.
+          const int chunk = lane & 7, col0 = 64 * (chunk >> 2) + 4 * (chunk & 3);
+          int to[4];  // rows of the item in Z, or of the slot; -1: past the last
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = row0 + row16 + 4 * k + (lane >> 3), rr = rt * P.tile_rows + r;
+            const int i = rr / P.share, head = kv * P.share + (rr - i * P.share);
+            to[k] = rr >= P.n_q * P.share ? -1 : whole ? i * P.h + head : r;
+          }
 #pragma unroll 1
           for (int cb = 0; cb < 4; ++cb) {
             // columns [16 cb, 16 cb + 16) of this half row's 64
@@ -1580,20 +1608,17 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
               sts128(stage + swz(lane & 15, half * 4 + k),
                      make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
             __syncwarp();
-            const int chunk = lane & 7, col = 64 * (chunk >> 2) + 16 * cb + 4 * (chunk & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int rho = 4 * k + (lane >> 3), r = row0 + row16 + rho;
-              const int rr = rt * P.tile_rows + r, i = rr / P.share, head = kv * P.share + (rr - i * P.share);
-              const uint4 o = lds128(stage + swz(rho, chunk));
-              if (rr >= P.n_q * P.share || col >= P.d_vh) continue;
+              const uint4 o = lds128(stage + swz(4 * k + (lane >> 3), chunk));
+              if (to[k] < 0 || col0 + 16 * cb >= P.d_vh) continue;
               if (whole)
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(P.Z) +
-                                          (((long long)cc.b * P.n_q + i) * P.h + head) * P.d_vh + col) =
+                                          ((long long)cc.b * P.n_q * P.h + to[k]) * P.d_vh + col0 + 16 * cb) =
                     make_uint2(pack_bf16x2(__uint_as_float(o.x), __uint_as_float(o.y)),
                                pack_bf16x2(__uint_as_float(o.z), __uint_as_float(o.w)));
               else
-                *reinterpret_cast<uint4*>(pz + (at * P.slot_rows + r) * P.d_vh + col) = o;
+                *reinterpret_cast<uint4*>(pz + (at * P.slot_rows + to[k]) * P.d_vh + col0 + 16 * cb) = o;
             }
             __syncwarp();
           }
@@ -1626,7 +1651,10 @@ mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s) {
   while (P.bt % box) box /= 2;
   if (!make_cache_maps(P, box, ROW)) return MHA_ERR_CUDA;
   P.ranges = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
-  P.tile_cost = P.tile_rows > 16 ? 3 : 2 + P.slot_rows / 4;
+  // What beginning and ending a tile costs, in groups, as measured: 16 rows
+  // (32 sequences of 4 drafted tokens): 6, 298 -> 236 us against none; a pair of
+  // slots writes 128 KB of sums: 4 to 6, 92 us against 95 with 3 (above).
+  P.tile_cost = P.tile_rows == 256 ? 5 : P.tile_rows == 128 ? 3 : 2 + P.slot_rows / 4;
   cudaError_t e;
   if (P.tile_rows > 16)
     e = launch(cache_attention_many_kernel, Many::THREADS, Many::SMEM, P, s);

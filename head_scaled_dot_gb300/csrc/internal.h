@@ -142,7 +142,7 @@ struct AppendArgs {
 };
 mha_status cache_append(const AppendArgs& a, mha_dtype dt, cudaStream_t s);
 
-// Attention over an 8-bit cache (attn_cache.cu).
+// Attention over an 8-bit cache (attn_cache.cu, attn_cache_tc.cu).
 struct CacheAttnArgs {
   const void* Q;
   const void* K_cache;
@@ -159,7 +159,7 @@ struct CacheAttnArgs {
   int causal_tail;
   float c;
 };
-size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_h, int d_vh);
+size_t cache_attention_workspace_bytes(int n_q, int h, int h_kv, int d_vh);
 mha_status cache_attention(const CacheAttnArgs& a, mha_dtype dt, cudaStream_t s);
 
 // Raises the dynamic shared-memory limit of `kernel` to `bytes` on the

@@ -713,7 +713,7 @@ mha_status mha_cache_append(const void* K, const void* V, const int64_t* slot_ma
 
 size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_kv, int d_h, int d_vh) {
   if (B <= 0 || n_q <= 0 || h <= 0 || h_kv <= 0 || h % h_kv || d_h <= 0 || d_vh <= 0) return 0;
-  return cache_attention_workspace_bytes(n_q, h, h_kv, d_h, d_vh);
+  return cache_attention_workspace_bytes(n_q, h, h_kv, d_vh);
 }
 
 mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V_cache,

@@ -533,8 +533,8 @@ MHA_API mha_status mha_cache_append(const void* K, const void* V, const int64_t*
 
 /*
  * Device scratch of mha_attention_cache, in bytes: the summaries of the pieces
- * that tiles of up to 16 query rows are cut into, at most two per warp of the
- * grid. It does not depend on B or on any length. 0 when an argument is
+ * that tiles of query rows are cut into, at most two per worker of the grid. It
+ * does not depend on B or on any length. 0 when an argument is
  * non-positive or h_kv does not divide h.
  */
 MHA_API size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_kv, int d_h,
@@ -558,12 +558,16 @@ MHA_API size_t mha_attention_cache_workspace_size(int B, int n_q, int h, int h_k
  *                        bytes, 256-byte aligned, contents on entry irrelevant;
  *                        calls that share it must not overlap on the GPU
  *
- * Scores, weights and sums in fp32; in the products the cache's numbers are
- * exact, bf16 queries too, and weights have 11 bits (22 with MHA_DTYPE_F32,
- * queries as well). Cache rows at positions >= total_len[b] are never read,
- * and a NaN in a row does not reach the query rows that do not see it.
- * Built for few query rows per key/value head (generated or drafted tokens):
- * 16 rows, n_q * h / h_kv, share one pass over the cache.
+ * Scores, statistics and sums in fp32. In the products fp32 queries and their
+ * weights have 22 bits; bf16 queries are exact (elements below 2^-13 of their
+ * row's largest lose bits) and their weights have 11 bits, or 8 for up to 16 of
+ * them per key/value head, n_q * h / h_kv, with head sizes up to 128. The
+ * cache's numbers are exact, and so are its scales, but for more than 16 rows
+ * with V_scale that are no powers of two, where a value has 10 bits. V_scale are
+ * not negative. Cache rows at positions >= total_len[b] do not matter, whatever
+ * they hold, and a NaN in a row does not reach the query rows that do not see
+ * it. Up to 16 rows per key/value head (generated or drafted tokens)
+ * the cache is streamed once, above that once for every 256 rows.
  *
  * MHA_ERR_INVALID_ARG for NULL pointers, non-positive sizes, h not a multiple
  * of h_kv, non-finite c; MHA_ERR_UNSUPPORTED for other head or block sizes

@@ -170,8 +170,8 @@ def test_attention_workspace_size(lib):
     size = mha.attention_cache_workspace_size
     assert size(0, 1, 8, 8, 64, 64) == 0 and size(1, 1, 8, 3, 64, 64) == 0
     assert size(1, 1, 8, 8, 128, 128) == size(1000, 1, 8, 8, 128, 128) > 0
-    # 16 rows share a summary slot: more rows need no more
-    assert size(1, 4, 32, 8, 128, 128) == size(1, 400, 32, 8, 128, 128)
+    # at most 256 rows share a summary slot: more need no more
+    assert size(1, 4, 32, 8, 128, 128) < size(1, 64, 32, 8, 128, 128) == size(1, 4000, 32, 8, 128, 128)
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_types(lib):

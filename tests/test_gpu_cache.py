@@ -17,15 +17,20 @@ Bounds. u = 2^-24 is fp32's half step. Each is a worst-case count of roundings:
              fp32 queries, bf16 ones of more than 128 columns: two fp16 or one,
                2^-22 or 2^-11; scaled by at least 2^9 (2^13, less up to 2^4
                between blocks' scales), so 2^-25 / 2^9 = 2^-34 N;
-             other bf16 queries: fp16, then hi + lo / 16 in e4m3, 2^-11 and the
-               2^-4 of hi times that of lo, 2^-8; scaled by at least 2^2 (2^7,
-               less 2^4 between blocks' scales, less 2^1 as the reference may be
-               above the largest weight), lo's smallest half is 2^-10 / 2^4, so
-               2^-16 N.
+             other bf16 queries, up to 16 rows per key/value head: fp16, then
+               hi + lo / 16 in e4m3, 2^-11 and the 2^-4 of hi times that of lo,
+               2^-8; scaled by at least 2^2 (2^7, less 2^4 between blocks'
+               scales, less 2^1 as the reference may be above the largest
+               weight), lo's smallest half is 2^-10 / 2^4, so 2^-16 N.
                Their query elements are hi + lo / 16 of a row whose largest is
                at least 2^7, exact but for lo's smallest half, 2^-14 of it,
-               2^-21 T on a score; with more than 16 rows per key/value head lo
-               is not scaled: 2^-10 / 2^7 = 2^-17 T
+               2^-21 T on a score
+             more rows: fp16 weights, 2^-11, scaled by 2^7, 2^-25 / 2^7 N; values
+               times their scale's ratio to a largest one, both rounded to fp16
+               unless powers of two, 2^-11 each (the ratio is at least 2^-4 and
+               an e4m3 number 2^-9: 2^-13 is not below fp16's normal numbers).
+               Query elements are scaled to a largest of at least 2^14:
+               2^-25 / 2^14 T
 """
 
 import numpy as np
@@ -398,8 +403,11 @@ def attention_bound(ref, parts, d, longest, dtype, rows=1):
     A, S, N, T = parts
     score = (d + 8) * 2 * U * S
     if dtype == "bf16" and d <= 128:
-        weight, floor = 2.0 ** -8 + 2.0 ** -11, 2.0 ** -16
-        score = score + T * (2.0 ** -21 if rows <= 16 else 2.0 ** -17)
+        if rows <= 16:
+            weight, floor, q = 2.0 ** -8 + 2.0 ** -11, 2.0 ** -16, 2.0 ** -21
+        else:
+            weight, floor, q = 3 * 2.0 ** -11, 2.0 ** -32, 2.0 ** -39
+        score = score + T * q
     else:
         weight, floor = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22, 2.0 ** -34
     return (HALF_STEP[dtype] * np.abs(ref) + floor * N
