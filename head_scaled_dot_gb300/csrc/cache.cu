@@ -233,7 +233,11 @@ __global__ void __launch_bounds__(RES_THREADS) release_kernel(const __grid_const
 // Bound: memory; each row is read once and its bytes are written once. A CTA
 // takes the rows of one block and head, of keys or of values, and keeps them in
 // registers between the maximum and the rounding (blocks of more than 32,768
-// elements are read a second time, from L2).
+// elements are read a second time, from L2). Rows without a slot are not read:
+// with them a prompt of 8192 rows and a shorter one, 16 heads of 128 in bf16,
+// took 31.1 us, without 25.5 (134 MB, 0.78 of the copy bandwidth). Fewer
+// registers for more CTAs an SM, or twice the threads with half the rows each,
+// were slower (31.9 to 42 and 32.2 to 36 us against the 31.1).
 
 struct AppendParams {
   const void* x[2];   // K, V: (B, h, n, d)
@@ -330,13 +334,18 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   grid_dep_launch_dependents();
   const int which = blockIdx.z & 1, b = blockIdx.z >> 1, head = blockIdx.y;
   const int64_t* slots = P.slot_map + (long long)b * P.n;
-  const int64_t first = __ldg(slots);
+  // Row blockIdx.x bt is in this part wherever the first one lies: where it has
+  // no slot only the rows before it can have one, and the others stay unread.
+  const int probe = min((long long)blockIdx.x * P.bt, P.n - 1ll);
+  const int64_t first = __ldg(slots), at_probe = __ldg(slots + probe);
   if (first < 0) return;  // no new rows
   const int off = (int)(first % P.bt);
   const int kept = blockIdx.x == 0 ? off : 0;  // rows that the block holds already
   const int row0 = blockIdx.x == 0 ? 0 : blockIdx.x * P.bt - off;  // first row of the part
   if (row0 >= P.n) return;
   const int d = P.d[which], vecs = d / 16, most = min(P.bt - kept, P.n - row0);
+  const int reach = at_probe < 0 ? min(probe - row0, most) : most;  // rows that may have a slot
+  if (reach <= 0) return;
   const T* x = static_cast<const T*>(P.x[which]) + (((long long)b * P.h + head) * P.n + row0) * d;
   // the rows, on their way while the slots are looked at
   Vec16<T> v[HELD > 0 ? HELD : 1];
@@ -344,10 +353,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
       const int e = threadIdx.x + k * THREADS;
-      if (e < most * vecs) v[k].load(x + (long long)e * 16); else v[k].zero();
+      if (e < reach * vecs) v[k].load(x + (long long)e * 16); else v[k].zero();
     }
   }
-  if (threadIdx.x == 0) s_rows = most;
+  if (threadIdx.x == 0) s_rows = reach;
   const int64_t slot0 = __ldg(slots + row0);
   if (slot0 < 0) return;  // past the item's last row
   const int64_t block = slot0 / P.bt;
