@@ -1,6 +1,7 @@
 // mha_api.cu - the C ABI (include/mha.h): argument checks, workspace layout,
 // dispatch of the three steps, device error word, TMA descriptor encoding.
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -702,7 +703,8 @@ mha_status mha_cache_append(const void* K, const void* V, const int64_t* slot_ma
   if (B <= 0 || n <= 0 || h <= 0 || d_h <= 0 || d_vh <= 0 || n_blocks <= 0 || block_tokens <= 0 ||
       !dtype_ok(dt))
     return MHA_ERR_INVALID_ARG;
-  if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > 32767 || h > 65535)
+  if (!cache_shape_ok(d_h, d_vh, block_tokens) || B > 32767 || h > 65535 ||
+      n > INT_MAX - MHA_MAX_BLOCK_TOKENS)  // (row numbers of whole blocks)
     return MHA_ERR_UNSUPPORTED;
   if (!aligned16(K) || !aligned16(V) || !aligned16(K_cache) || !aligned16(V_cache))
     return MHA_ERR_UNSUPPORTED;
@@ -735,6 +737,7 @@ mha_status mha_attention_cache(const void* Q, const void* K_cache, const void* V
   // tiles of rows (and what tiles cost beside them): 32-bit counts
   const long long rows = (long long)n_q * (h / h_kv), tiles = h_kv * ((rows + 15) / 16);
   if (!fits(max_blocks, block_tokens, 1) || !fits(n_blocks, h_kv, 1) || !fits((long long)B, n_q, h) ||
+      rows > INT_MAX - 256 ||  // (row numbers of whole tiles)
       !fits((long long)B * max_blocks, block_tokens / 16 + 8, tiles))
     return MHA_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(Z))

@@ -131,6 +131,7 @@ def _append(lib, **kw):
     (dict(dt=7), INVALID), (dict(d_h=72), UNSUPPORTED), (dict(d_vh=272), UNSUPPORTED),
     (dict(bt=24), UNSUPPORTED), (dict(bt=1040), UNSUPPORTED), (dict(B=32768), UNSUPPORTED),
     (dict(K=4104), UNSUPPORTED), (dict(Vc=20481), UNSUPPORTED),
+    (dict(n=(1 << 31) - 100), UNSUPPORTED),
 ])
 def test_append_refusals(lib, kw, code):
     assert _append(lib, **kw) == code
@@ -158,6 +159,7 @@ def _attend(lib, **kw):
     (dict(d_h=24), UNSUPPORTED), (dict(d_vh=272), UNSUPPORTED), (dict(bt=8), UNSUPPORTED),
     (dict(bt=2048), UNSUPPORTED), (dict(B=1025), UNSUPPORTED),
     (dict(max_blocks=1 << 28), UNSUPPORTED), (dict(B=1000, max_blocks=1 << 22), UNSUPPORTED),
+    (dict(B=1, h=1, h_kv=1, max_blocks=1, n_q=(1 << 31) - 100), UNSUPPORTED),
     (dict(n_q=1 << 28), UNSUPPORTED), (dict(Q=4104), UNSUPPORTED), (dict(Z=36872), UNSUPPORTED),
     (dict(ws=None), WORKSPACE), (dict(ws=(1 << 20) + 16), WORKSPACE), (dict(ws_bytes=4096), WORKSPACE),
 ])
