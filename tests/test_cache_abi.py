@@ -104,6 +104,7 @@ def _reserve(lib, release=False, **kw):
     (dict(n_out=16384), INVALID), (dict(total=4096), INVALID), (dict(total=8192), INVALID),
     (dict(B=1025), UNSUPPORTED), (dict(bt=1025), UNSUPPORTED),
     (dict(max_blocks=1 << 28, bt=16), UNSUPPORTED),
+    (dict(max_blocks=1 << 22, bt=16, B=1024), UNSUPPORTED),
 ])
 def test_pool_refusals(lib, release, kw, code):
     assert _reserve(lib, release, **kw) == code

@@ -474,6 +474,8 @@ def test_attention_of_the_largest_batch_and_of_none():
     cache = Cache(3 * 1024, 1, 16, 32, 32, 11)
     attend_and_check(cache, total, None, 1, 2, 32, 32, "bf16", True, 12)
     attend_and_check(cache, [0] * 5, None, 2, 2, 32, 32, "bf16", True, 13)
+    attend_and_check(cache, total, None, 9, 2, 32, 32, "bf16", True, 14)
+    attend_and_check(cache, [0] * 5, None, 200, 1, 32, 32, "bf16", True, 15)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -642,19 +644,20 @@ def test_offsets_past_32_bits():
     assert (np.abs(f64(Z) - ref) <= attention_bound(ref, parts, d_h, n, "bf16")).all()
 
 
-def test_calls_on_another_stream_and_two_graphs_that_share_a_workspace():
+@pytest.mark.parametrize("n_q", [2, 40, 150])
+def test_calls_on_another_stream_and_two_graphs_that_share_a_workspace(n_q):
     cache = Cache(40, 2, 32, 64, 64, 71)
     total, h = [600, 500], 2
     table = ints(table_of(total, 32, 40, 20, 7).tolist())
     lens = ints(total)
-    Q = [torch.randn((2, h, 2, 64), device="cuda").bfloat16() for _ in range(2)]
+    Q = [torch.randn((2, h, n_q, 64), device="cuda").bfloat16() for _ in range(2)]
     want = [mha.attention_cache(q, *cache.args, table, lens, 0.125, causal_tail=True) for q in Q]
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     got = mha.attention_cache(Q[0], *cache.args, table, lens, 0.125, causal_tail=True, stream=side)
     side.synchronize()
     assert torch.equal(got, want[0])
-    ws = torch.empty(mha.attention_cache_workspace_size(2, 2, h, 2, 64, 64), dtype=torch.uint8,
+    ws = torch.empty(mha.attention_cache_workspace_size(2, n_q, h, 2, 64, 64), dtype=torch.uint8,
                      device="cuda")
     outs, graphs = [torch.empty_like(w) for w in want], []
     for q, o in zip(Q, outs):
