@@ -32,7 +32,7 @@
 //     subset of fp16 and bf16's 8 bits, scaled by a power of two per row, fit in
 //     its 11. (With the bytes as operands and hi and lo of queries and weights
 //     the products were twice as many, each as long as one in fp16, and the
-//     weights cost two conversions more: 145 us against 92 for 2 x 4 key/value
+//     weights cost two conversions more: 145 us against 89 for 2 x 4 key/value
 //     heads of 2048 rows over 6000 keys, d = 128. Rows of up to 128 take as
 //     long either way.) With at most 128 rows the slots take the groups of keys
 //     in turn and their sums are added at the end.
@@ -40,6 +40,8 @@
 // Against the mma.sync kernel of attn_cache.cu, which these replaced for bf16:
 // its m16n8k16 products alone took 512 cycles per 32 keys and SM, more than
 // HBM's share of 370.
+#include <type_traits>
+
 #include "attn_cache.cuh"
 
 namespace mha {
@@ -959,8 +961,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 // ---------------------------------------------------------------------------
 // Many rows: S = Q K^T, z = P V
 //
-// What bounds it: 92 us for 2 sequences x 4 key/value heads x 2048 query rows
-// (512 new ones of 4 heads each) over 6000 keys, d = 128, 496 TFLOP/s; the
+// What bounds it: 89 us for 2 sequences x 4 key/value heads x 2048 query rows
+// (512 new ones of 4 heads each) over 6000 keys, d = 128, 509 TFLOP/s; the
 // products alone are 24 us. A group of keys for a pair of slots takes about
 // 4600 cycles, 3400 of them the eight softmax warps (for 128 rows 650 for the
 // loads and maxima and 950 for the weights, on its own 930 together; products
@@ -1252,8 +1254,10 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         }
         __syncwarp();
       };
-      // times g[0] for the first 16 of the warp's 32 rows, g[1] for the others
-      auto write = [&](uint32_t dst, const __half2 (&g)[2]) {
+      // scaled: times g[0] for the first 16 of the warp's 32 rows, g[1] for the
+      // others. (Without the products for keys 92 -> 89 us. Converting ahead of
+      // the waits for the operand's readers took 95 to 100: too many registers.)
+      auto write = [&](uint32_t dst, const __half2 (&g)[2], auto scaled) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const Piece p(warp & 3, lane, i);
@@ -1262,8 +1266,10 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             o[k] = k & 1 ? e4m3_hi(x[k / 2]) : e4m3_lo(x[k / 2]);
-            const __half2 v = __hmul2(reinterpret_cast<const __half2&>(o[k]), g[i / 4]);
-            o[k] = reinterpret_cast<const uint32_t&>(v);
+            if constexpr (decltype(scaled)::value) {
+              const __half2 v = __hmul2(reinterpret_cast<const __half2&>(o[k]), g[i / 4]);
+              o[k] = reinterpret_cast<const uint32_t&>(v);
+            }
           }
           const uint32_t to = dst + p.panel * F::PANEL;
           sts128(to + swz(p.row, 2 * p.col), make_uint4(o[0], o[1], o[2], o[3]));
@@ -1275,8 +1281,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
       read(src);
       if (n > 0) cache_wait(k_free + last, last_par, ctl);  // the operand's last readers
       __syncwarp();
-      const __half2 one = __float2half2_rn(1.f);
-      write(base + F::KEY_AT, {one, one});
+      write(base + F::KEY_AT, {}, std::false_type());
       if (lane == 0) mbar_arrive(k_full + (n & 1));
 
       if (masked) {
@@ -1311,7 +1316,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         const uint32_t times = held ? rounds[1] : rounds[0];
         if (times > 0) cache_wait(v_free + held, (times - 1) & 1, ctl);
         __syncwarp();
-        write(base + (pair || (n & 1) == 0 ? F::VALUE_AT : F::Q_AT + F::OPERAND), g);
+        write(base + (pair || (n & 1) == 0 ? F::VALUE_AT : F::Q_AT + F::OPERAND), g, std::true_type());
         before = n & 1;
         if (lane == 0) mbar_arrive(v_full + before);
         if (before) ++rounds[1]; else ++rounds[0];
@@ -1454,6 +1459,19 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           tc_fence_after();
           const uint32_t s_at = tmem + lanes + F::S_COL + t * 128;
           const uint32_t found = meta->found;
+          if (__all_sync(0xffffffffu, cur.limit < kb)) {
+            // None of the warp's rows sees a key of the group. (2048 new rows over
+            // 4096 keys: 78 -> 72 us.)
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = 0u;
+            tmem_st_x2_16<32>(s_at, w);
+            tmem_st_x2_16<32>(s_at + 16, w);
+            const float owed = cur.owed;
+            cur.owed = 1.f;
+            give(owed * to);
+            continue;
+          }
           uint32_t x[64];
           tmem_ld_x2_64<64>(s_at, x);
           float ks[4], least = 1.f;
