@@ -419,6 +419,7 @@ def _cache_type(t):
 # The current stream's handle of a device, without the stream object around it
 # (which takes longer to make than a small kernel runs).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _queue(t, stream):
@@ -427,7 +428,7 @@ def _queue(t, stream):
     index = t.get_device()
     if index < 0:
         raise ValueError("CUDA tensors expected, got a tensor on %s" % t.device)
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError("tensors on %s, but the current device is %d"
                          % (t.device, torch.cuda.current_device()))
     if stream is not None:
