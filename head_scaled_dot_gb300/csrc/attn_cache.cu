@@ -168,12 +168,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  scan_groups<CA_THREADS, S::SK>(P, first, nullptr, warp_sums);
-  const Ranges ranges(P, first[P.B]);
-  const int unit = ranges.unit, w = blockIdx.x * CA_WARPS + warp;
+  using R = Ranges<false, S::SK>;
+  scan_groups<CA_THREADS, S::SK, false>(P, first, nullptr, nullptr, warp_sums);
+  const R ranges(P, first[P.B]);
+  const int w = blockIdx.x * CA_WARPS + warp;
   Cursor cc, past;  // what is computed; the next range's first
-  const int g0 = ranges.begin(w, first, P.B, cc);
-  int left = ranges.begin(w + 1, first, P.B, past) - g0, load_left = left;
+  const int g0 = ranges.begin(P, w, first, nullptr, nullptr, cc);
+  int left = ranges.begin(P, w + 1, first, nullptr, nullptr, past) - g0, load_left = left;
   if (left <= 0) return;
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
   const uint32_t ring = smem_u32(smem) + warp * S::N * S::BYTES;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     put_scales();
     if (load_left <= 0) return;
     issue(stage);
-    if (--load_left > 0 && advance(lc, first, P.B, unit)) place();
+    if (--load_left > 0 && advance<R>(P, lc, first)) place();
   };
 #pragma unroll 1
   for (int k = 0; k < S::N - 1; ++k) load_next(k);
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     fold(stage);
     begins = cc.gi == cc.ng - 1 || left == 1;
     if (begins) end_piece();
-    advance(cc, first, P.B, unit);
+    advance<R>(P, cc, first);
     if (++stage == S::N) {
       stage = 0;
       parity ^= 1;
@@ -684,26 +685,26 @@ __global__ void __launch_bounds__(CM_THREADS) cache_merge_kernel(const __grid_co
   const int i = (int)(bi % P.n_q), b = (int)(bi / P.n_q);
   const int kv = head / P.share, r = i * P.share + head % P.share;
   const int pr = kv * P.tiles + r / P.tile_rows, row = r % P.tile_rows;
-  const int ng = P.first[b + 1] - P.first[b];
   T* out = static_cast<T*>(P.Z) + (bi * P.h + head) * P.d_vh + col;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
   bool bad;
   const Item it = item_of(P, b, bad);
+  const Ranges<true, 128> ranges(P, P.first[P.B]);  // (128 keys a group where tiles' numbers differ)
+  int ng;
+  const int base = ranges.place(P, P.first, it, b, pr, ng);
   if (ng > 0) {
-    const Ranges ranges(P, P.first[P.B]);
-    const int w0 = ranges.owner(P.first, b, pr, 0, ng), w1 = ranges.owner(P.first, b, pr, ng - 1, ng);
+    const int w0 = ranges.owner(base), w1 = ranges.owner(base + ng - 1);
     if (w0 == w1) return;
     // Of the tile's ranges the first has it from its first group on (slot 2 w
     // + 1); the others come upon it in the middle (slot 2 w), but for those
     // that have no group at all, as when there are more ranges than groups.
-    const int cost = (P.first[b] + ranges.cost * b) * ranges.unit + pr * (ng + ranges.cost) + ranges.cost;
     const float* ml = P.part;
     const float* pz = P.part + 2ll * 2 * P.ranges * P.slot_rows;
 #pragma unroll 2
     for (int w = w0 + (ROWS ? 0 : pg); w <= w1; w += ROWS ? 1 : PG) {
       // its units [u, v) of the costs, as the tile's groups
-      const int u = w * ranges.per + min(w, ranges.more) - cost;
+      const int u = w * ranges.per + min(w, ranges.more) - base;
       const int v1 = u + ranges.per + (w < ranges.more ? 1 : 0);
       if (max(v1, 0) <= max(u, 0)) continue;
       const long long at = (2ll * w + (u <= 0 ? 1 : 0)) * P.slot_rows + row;

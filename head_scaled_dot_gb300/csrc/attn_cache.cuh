@@ -37,6 +37,8 @@ struct CacheAttnParams {
   int causal_tail;
   int ranges;           // the list of groups is cut into so many ranges
   int tile_cost;        // what a tile costs beside its groups, in groups
+  int per_tile;         // tiles have groups up to what their last row sees, else all of them
+  int tile_new;         // new rows per tile where heads do not cross tiles, else 0 (divisions then)
   float cl2;            // c log2(e)
   uint64_t limit_ns;    // bounded waits give up after this long
 };
@@ -61,12 +63,24 @@ __device__ __forceinline__ Item item_of(const CacheAttnParams& P, int b, bool& b
   return Item{min(max(t, 0), most), min(max(f, 0), P.n_q)};
 }
 
-// first[b], b = 0 .. B: groups of SK keys per tile of rows before batch item
-// b; totals[b] (unless null): its keys. Every CTA computes them; the first one
-// leaves them in the workspace and reports lengths out of bounds. All threads
-// of the CTA.
-template <int THREADS, int SK>
-__device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first, int* totals,
+// Groups of SK keys of tile rt of an item's rows, with P.per_tile: up to what
+// its last row sees, none for a tile of padding. (Against all groups of the
+// sequence for every tile: 512 new rows over 6000 keys 89.5 -> 78.8 us, 2048
+// over 4096 72 -> 65.6; with divisions only, 83.8 and 78.)
+__device__ __forceinline__ int tile_groups(const CacheAttnParams& P, int total, int fresh, int rt, int SK) {
+  const int begin = P.tile_new ? rt * P.tile_new : rt * P.tile_rows / P.share;
+  const int end = P.tile_new ? begin + P.tile_new : ((rt + 1) * P.tile_rows - 1) / P.share + 1;
+  const int keys = total - fresh + min(end, fresh);  // (fresh is at most n_q)
+  return begin >= fresh || keys <= 0 ? 0 : (unsigned)(keys + SK - 1) / SK;
+}
+
+// first[b], b = 0 .. B: groups of SK keys before batch item b, per tile of rows
+// (with P.per_tile per key/value head, all its tiles together); totals[b],
+// news[b] (unless null): its keys and new rows. Every CTA computes them; the
+// first one leaves them in the workspace and reports lengths out of bounds. All
+// threads of the CTA.
+template <int THREADS, int SK, bool PT>
+__device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first, int* totals, int* news,
                                             int* warp_sums) {
   constexpr int PER = (MHA_MAX_PADDED_BATCH + THREADS - 1) / THREADS;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -79,8 +93,14 @@ __device__ __forceinline__ void scan_groups(const CacheAttnParams& P, int* first
       bool bad;
       const Item it = item_of(P, b, bad);
       if (bad && blockIdx.x == 0 && P.err) atomicCAS(P.err, 0, MHA_ERR_INVALID_ARG);
-      if (it.fresh > 0) n[k] = (it.total + SK - 1) / SK;
+      if (it.fresh > 0) {
+        if (PT && P.per_tile)
+          for (int t = 0; t < P.tiles; ++t) n[k] += tile_groups(P, it.total, it.fresh, t, SK);
+        else
+          n[k] = (it.total + SK - 1) / SK;
+      }
       if (totals) totals[b] = it.total;
+      if (news) news[b] = it.fresh;
     }
     sum += n[k];
   }
@@ -118,56 +138,111 @@ struct Cursor {
 
 // How the list is cut into ranges. Beginning and ending a tile costs about as
 // much as P.tile_cost groups, so equal shares are of costs: a tile's groups
-// come after tile_cost units of their own, item b's first tile has
-// (first[b] + tile_cost b) unit of them before it (unit: tiles per item), and
-// range w begins at w / ranges of them all. (With shares of groups alone a CTA
-// that got ten short tiles took 307 us where the median took 226.)
+// come after tile_cost units of their own, and range w begins at w / ranges of
+// them all. Item b has `unit` parts of first[b + 1] - first[b] groups and `cost`
+// more each: its tiles, or with P.per_tile its key/value heads. (With shares of
+// groups alone a CTA that got ten short tiles took 307 us where the median took
+// 226.)
+// PT: tiles may have groups of their own number (P.per_tile), of SK keys.
+template <bool PT, int SK>
 struct Ranges {
   int unit, cost, n, per, more;  // the first `more` ranges have per + 1 units
   __device__ __forceinline__ Ranges(const CacheAttnParams& P, int groups)
-      : unit(P.h_kv * P.tiles), cost(P.tile_cost), n(P.ranges) {
+      : unit(PT && P.per_tile ? P.h_kv : P.h_kv * P.tiles),
+        cost(PT && P.per_tile ? P.tile_cost * P.tiles : P.tile_cost),
+        n(P.ranges) {
     const int all = groups * unit + cost * unit * P.B;
     per = all / n;
     more = all - per * n;
   }
   // The first group of range w: its cursor, and its number in the list. (w = n:
-  // the end.)
-  __device__ __forceinline__ int begin(int w, const int* first, int B, Cursor& c) const {
-    const int at = w * per + min(w, more);
+  // the end.) totals and news with PT only.
+  __device__ __forceinline__ int begin(const CacheAttnParams& P, int w, const int* first, const int* totals,
+                                       const int* news, Cursor& c) const {
+    const int at = w * per + min(w, more), B = P.B;
     int lo = 0, hi = B;  // the last item that starts at or before it
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
       if ((first[mid] + cost * mid) * unit <= at) lo = mid; else hi = mid - 1;
     }
+    const int item = lo;
     while (lo < B && first[lo + 1] == first[lo]) ++lo;  // (in an empty one: on to the next group)
     c.b = lo;
     c.pr = c.gi = 0;
     c.ng = lo < B ? first[lo + 1] - first[lo] : 1;
-    const int in = at - (first[lo] + cost * lo) * unit;
-    if (lo < B && in > 0) {
-      c.pr = in / (c.ng + cost);
-      c.gi = max(0, in - c.pr * (c.ng + cost) - cost);
+    if (lo == B) return first[B] * unit;
+    const int size = c.ng + cost;
+    int in = lo == item ? at - (first[lo] + cost * lo) * unit : 0;
+    if (!(PT && P.per_tile)) {
+      if (in > 0) {
+        c.pr = in / size;
+        c.gi = max(0, in - c.pr * size - cost);
+      }
+      return first[lo] * unit + c.pr * c.ng + c.gi;
     }
-    return first[lo] * unit + c.pr * c.ng + c.gi;
+    // along the head's tiles; from a place in an empty one on to the next group
+    const int kv = in / size;
+    int number = first[lo] * unit + kv * c.ng;
+    in -= kv * size;
+    for (int t = 0; t < P.tiles; ++t) {
+      const int g = tile_groups(P, totals[lo], news[lo], t, SK);
+      if (g > 0 && in < P.tile_cost + g) {
+        c.pr = kv * P.tiles + t;
+        c.gi = max(0, in - P.tile_cost);
+        c.ng = g;
+        return number + c.gi;
+      }
+      in = max(0, in - P.tile_cost - g);
+      number += g;
+    }
+    c.pr = (kv + 1) * P.tiles - 1;  // past the head's last group
+    c.gi = 0;
+    c.ng = 1;
+    next_tile(P, c, first, totals, news);
+    return number;
   }
-  // The range that has the group `gi` of a tile.
-  __device__ __forceinline__ int owner(const int* first, int b, int pr, int gi, int ng) const {
-    const int at = (first[b] + cost * b) * unit + pr * (ng + cost) + cost + gi;
+  // Where the tile's first group is in the costs; g: its groups.
+  __device__ __forceinline__ int place(const CacheAttnParams& P, const int* first, const Item& it, int b, int pr,
+                                       int& g) const {
+    const int ng = first[b + 1] - first[b], at = (first[b] + cost * b) * unit;
+    g = ng;
+    if (!(PT && P.per_tile)) return at + pr * (ng + cost) + cost;
+    const int kv = pr / P.tiles, rt = pr - kv * P.tiles;
+    int before = 0;
+    for (int t = 0; t < rt; ++t) before += P.tile_cost + tile_groups(P, it.total, it.fresh, t, SK);
+    g = ng > 0 ? tile_groups(P, it.total, it.fresh, rt, SK) : 0;
+    return at + kv * (ng + cost) + before + P.tile_cost;
+  }
+  // The range that has unit `at` of the costs.
+  __device__ __forceinline__ int owner(int at) const {
     const int big = more * (per + 1);
     return at < big ? at / (per + 1) : more + (at - big) / per;
+  }
+  // On to the next tile that has groups.
+  static __device__ __forceinline__ void next_tile(const CacheAttnParams& P, Cursor& c, const int* first,
+                                                   const int* totals, const int* news) {
+    c.gi = 0;
+#pragma unroll 1
+    do {
+      if (++c.pr == P.h_kv * P.tiles) {
+        c.pr = 0;
+        do {
+          ++c.b;
+        } while (c.b < P.B && first[c.b + 1] == first[c.b]);
+      }
+      c.ng = c.b >= P.B         ? 1
+             : PT && P.per_tile ? tile_groups(P, totals[c.b], news[c.b], c.pr % P.tiles, SK)
+                                : first[c.b + 1] - first[c.b];
+    } while (c.ng == 0);
   }
 };
 
 // True when the cursor has moved to another tile.
-__device__ __forceinline__ bool advance(Cursor& c, const int* first, int B, int unit) {
+template <class R>
+__device__ __forceinline__ bool advance(const CacheAttnParams& P, Cursor& c, const int* first,
+                                        const int* totals = nullptr, const int* news = nullptr) {
   if (++c.gi < c.ng) return false;
-  c.gi = 0;
-  if (++c.pr < unit) return true;
-  c.pr = 0;
-  do {
-    ++c.b;
-  } while (c.b < B && first[c.b + 1] == first[c.b]);
-  c.ng = c.b < B ? first[c.b + 1] - first[c.b] : 1;
+  R::next_tile(P, c, first, totals, news);
   return true;
 }
 

@@ -300,9 +300,9 @@ __device__ __forceinline__ void mend_values(uint32_t src, int row, bool seen, in
 // the groups for itself. A stage is full after an arrival of each for its tiles
 // and the tiles' bytes; there_meta gets one for the scales (with NM = NS it is
 // the stage's barrier too).
-template <int NS, int NM>
+template <int NS, int NM, class R>
 __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* first,
-                                          const int* totals, int unit, Cursor lc, int steps,
+                                          const int* totals, const int* news, Cursor lc, int steps,
                                           uint32_t stages, Meta* metas, uint64_t* full, uint64_t* there_meta,
                                           uint64_t* empty, const WaitCtl& ctl) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -394,7 +394,7 @@ __device__ __forceinline__ void fill_ring(const CacheAttnParams& P, const int* f
     } else {
       tile += STAGE;
     }
-    if (advance(lc, first, P.B, unit)) {
+    if (advance<R>(P, lc, first, totals, news)) {
       if (n + 1 < steps) place();
     } else {
       j += dj;
@@ -501,22 +501,23 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 
   grid_dep_wait();
   grid_dep_launch_dependents();
-  scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
+  using R = Ranges<false, KEYS>;
+  scan_groups<F::THREADS, KEYS, false>(P, first, totals, nullptr, warp_sums);
 
   // this CTA's range: where it begins, and its groups (found by one thread of
   // two warps)
   if ((threadIdx.x & ~32u) == 0) {
     const int k = threadIdx.x >> 5;
     Cursor c;
-    bounds[k] = Ranges(P, first[P.B]).begin(blockIdx.x + k, first, P.B, c);
+    bounds[k] = R(P, first[P.B]).begin(P, blockIdx.x + k, first, nullptr, nullptr, c);
     if (k == 0) start = c;
   }
   __syncthreads();
-  const int unit = P.h_kv * P.tiles, steps = bounds[1] - bounds[0];
+  const int steps = bounds[1] - bounds[0];
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (steps > 0 && (warp == 0 || warp == 2)) {
-    fill_ring<F::STAGES, F::STAGES>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full, full,
+    fill_ring<F::STAGES, F::STAGES, R>(P, first, totals, nullptr, start, steps, smem_u32(smem), metas, full, full,
                                     empty, ctl);
   } else if (steps > 0 && warp == 1 && lane == 0) {
     // ---- scores ----
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         }
       }
       cc.gi = cc.ng - 1;
-      if (n < steps) advance(cc, first, P.B, unit);
+      if (n < steps) advance<R>(P, cc, first);
     }
     umma_commit(done);  // what is in flight ends before tensor memory is given back
     wait_in_flight(done, 0);
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         pv_other = other;
       }
       cc.gi = cc.ng - 1;
-      if (n < steps) advance(cc, first, P.B, unit);
+      if (n < steps) advance<R>(P, cc, first);
     }
     umma_commit(done + 1);
     wait_in_flight(done + 1, 0);
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
       // the next tile: its item and its queries are on their way from here on
       Cursor nc = cc;
       nc.gi = nc.ng - 1;
-      if (n1 < steps) advance(nc, first, P.B, unit);
+      if (n1 < steps) advance<R>(P, nc, first);
       const Item next = item_of(P, nc.b < P.B ? nc.b : cc.b, bad);
       if (grp == 1 && n1 < steps) fetch_q(nc);
       if (grp == 0 && tid < F::ROWS * 4)
@@ -961,8 +962,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
 // ---------------------------------------------------------------------------
 // Many rows: S = Q K^T, z = P V
 //
-// What bounds it: 89 us for 2 sequences x 4 key/value heads x 2048 query rows
-// (512 new ones of 4 heads each) over 6000 keys, d = 128, 509 TFLOP/s; the
+// What bounds it: 79 us for 2 sequences x 4 key/value heads x 2048 query rows
+// (512 new ones of 4 heads each) over 6000 keys, d = 128, 579 TFLOP/s; the
 // products alone are 24 us. A group of keys for a pair of slots takes about
 // 4600 cycles, 3400 of them the eight softmax warps (for 128 rows 650 for the
 // loads and maxima and 950 for the weights, on its own 930 together; products
@@ -997,7 +998,8 @@ struct Many {
   static constexpr int QF_AT = LIM_AT + 2 * ROWS * 4;
   static constexpr int FIRST_AT = QF_AT + 2 * ROWS * 4;
   static constexpr int TOTAL_AT = FIRST_AT + (MHA_MAX_PADDED_BATCH + 8) * 4;
-  static constexpr int BAR_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
+  static constexpr int NEW_AT = TOTAL_AT + MHA_MAX_PADDED_BATCH * 4;
+  static constexpr int BAR_AT = NEW_AT + MHA_MAX_PADDED_BATCH * 4;
   static constexpr int SMEM = 1024 + BAR_AT + 288;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
@@ -1072,6 +1074,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
   float* qf_s = reinterpret_cast<float*>(smem + F::QF_AT);
   int* first = reinterpret_cast<int*>(smem + F::FIRST_AT);
   int* totals = reinterpret_cast<int*>(smem + F::TOTAL_AT);
+  int* news = reinterpret_cast<int*>(smem + F::NEW_AT);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::BAR_AT);  // [STAGES] bytes there
   uint64_t* empty = full + F::STAGES;    // [STAGES] bytes read
   uint64_t* meta_full = empty + F::STAGES;  // [METAS] scales there
@@ -1133,23 +1136,24 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
 
   grid_dep_wait();
   grid_dep_launch_dependents();
-  scan_groups<F::THREADS, KEYS>(P, first, totals, warp_sums);
+  using R = Ranges<true, KEYS>;
+  scan_groups<F::THREADS, KEYS, true>(P, first, totals, news, warp_sums);
 
   // this CTA's range: where it begins, and its groups (found by one thread of
   // two warps)
   if ((threadIdx.x & ~32u) == 0) {
     const int k = threadIdx.x >> 5;
     Cursor c;
-    bounds[k] = Ranges(P, first[P.B]).begin(blockIdx.x + k, first, P.B, c);
+    bounds[k] = R(P, first[P.B]).begin(P, blockIdx.x + k, first, totals, news, c);
     if (k == 0) start = c;
   }
   __syncthreads();
-  const int unit = P.h_kv * P.tiles, steps = bounds[1] - bounds[0];
+  const int steps = bounds[1] - bounds[0];
   const WaitCtl ctl{P.err, &abort_flag, P.limit_ns};
 
   if (warp < F::CONVERT_AT / 32) {
     if (steps > 0 && (warp == 0 || warp == 2)) {
-      fill_ring<F::STAGES, F::METAS>(P, first, totals, unit, start, steps, smem_u32(smem), metas, full,
+      fill_ring<F::STAGES, F::METAS, R>(P, first, totals, news, start, steps, smem_u32(smem), metas, full,
                                      meta_full, empty, ctl);
     } else if (steps > 0 && lane == 0) {
       // ---- products of slot t ----
@@ -1204,7 +1208,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           } while (todo);
           if (!ok) break;
         }
-        if (advance(cc, first, P.B, unit)) fresh = true;
+        if (advance<R>(P, cc, first, totals, news)) fresh = true;
       }
       umma_commit(done + t);  // the products in flight end before tensor memory is given back
       wait_in_flight(done + t, 0);
@@ -1322,7 +1326,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         if (before) ++rounds[1]; else ++rounds[0];
       } while (todo);
       begins = ends;
-      advance(cc, first, P.B, unit);
+      advance<R>(P, cc, first, totals, news);
     }
   } else {
     // ---- softmax ----
@@ -1460,8 +1464,8 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
           const uint32_t s_at = tmem + lanes + F::S_COL + t * 128;
           const uint32_t found = meta->found;
           if (__all_sync(0xffffffffu, cur.limit < kb)) {
-            // None of the warp's rows sees a key of the group. (2048 new rows over
-            // 4096 keys: 78 -> 72 us.)
+            // None of the warp's rows sees a key of the group: the last ones of a
+            // tile, for its first rows.
             uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) w[k] = 0u;
@@ -1645,7 +1649,7 @@ __global__ void __launch_bounds__(Many::THREADS, 1)
         named_sync(1, NST);  // before the next tile's queries come
         tc_fence_before();
       }
-      if (n < steps) advance(cc, first, P.B, unit);
+      if (n < steps) advance<R>(P, cc, first, totals, news);
     }
   }
   tc_fence_before();
@@ -1669,9 +1673,13 @@ mha_status launch_cache_attention_tc(CacheAttnParams& P, cudaStream_t s) {
   while (P.bt % box) box /= 2;
   if (!make_cache_maps(P, box, ROW)) return MHA_ERR_CUDA;
   P.ranges = num_sms() < CA_MAX_CTAS ? num_sms() : CA_MAX_CTAS;
+  // Rows that are the last of their sequence see up to themselves, so a tile
+  // needs the groups up to what its last row sees.
+  P.per_tile = P.causal_tail && P.tiles > 1;
+  P.tile_new = P.tile_rows % P.share ? 0 : P.tile_rows / P.share;
   // What beginning and ending a tile costs, in groups, as measured: 16 rows
   // (32 sequences of 4 drafted tokens): 6, 298 -> 236 us against none; a pair of
-  // slots writes 128 KB of sums: 4 to 6, 92 us against 95 with 3 (above).
+  // slots writes 128 KB of sums: 5, 78.8 us against 81.6 with 3 and 80.6 with 8.
   P.tile_cost = P.tile_rows == 256 ? 5 : P.tile_rows == 128 ? 3 : 2 + P.slot_rows / 4;
   cudaError_t e;
   if (P.tile_rows > 16)

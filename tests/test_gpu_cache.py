@@ -457,6 +457,8 @@ ATTEND = [
     ([5000, 700], [70, 64], 70, 16, 4, 128, 112, 32, "bf16", True),
     ([900, 2500], [64, 1], 64, 2, 1, 64, 48, 16, "bf16", True),      # one tile of rows exactly
     ([900, 2500], None, 129, 1, 1, 80, 128, 16, "bf16", False),      # one row past it
+    ([600, 0, 130, 2000], [600, 0, 400, 257], 600, 3, 1, 64, 64, 16, "bf16", True),  # heads across tiles
+    ([1500, 1], [1400, 1], 1400, 2, 2, 32, 32, 32, "bf16", True),    # most tiles see few keys
 ]
 
 
