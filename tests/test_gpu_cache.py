@@ -681,6 +681,25 @@ def test_calls_on_another_stream_and_two_graphs_that_share_a_workspace(n_q):
     assert torch.equal(outs[0], now) and not torch.equal(now, want[0])
 
 
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own, few and many rows, many times over."""
+    cache = Cache(80, 2, 64, 128, 128, 73)
+    total, h = [2400, 2300], 4
+    table, lens = ints(table_of(total, 64, 80, 38, 9).tolist()), ints(total)
+    Q = [torch.randn((2, h, n, 128), device="cuda").bfloat16() for n in (1, 8, 40, 200)]
+    want = [mha.attention_cache(q, *cache.args, table, lens, 0.09, causal_tail=True) for q in Q]
+    torch.cuda.synchronize()
+    err, streams, got = word(), [torch.cuda.Stream() for _ in Q], [[] for _ in Q]
+    for _ in range(20):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(mha.attention_cache(Q[k], *cache.args, table, lens, 0.09,
+                                                  causal_tail=True, dev_error=err))
+    torch.cuda.synchronize()
+    assert mha.get_device_error(err) == OK
+    assert all(torch.equal(z, want[k]) for k in range(len(Q)) for z in got[k])
+
+
 # ---------------------------------------------------------------------------
 # A run of them together
 # ---------------------------------------------------------------------------
